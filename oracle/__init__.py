@@ -75,6 +75,15 @@ def _load():
         lib.oracle_w8a8_matmul.argtypes = [p, p, i64, p, p, i64, i64, p, p]
         lib.oracle_w8a8_mul_mat.restype = ctypes.c_int
         lib.oracle_w8a8_mul_mat.argtypes = [p, p, i64, i64, p, i64, p, p]
+        ci = ctypes.c_int
+        lib.oracle_kv8_append.restype = None
+        lib.oracle_kv8_append.argtypes = [p, p, p]
+        lib.oracle_kv8_read.restype = None
+        lib.oracle_kv8_read.argtypes = [p, p, p]
+        lib.oracle_kv8_attention.restype = None
+        lib.oracle_kv8_attention.argtypes = [p, p, i64, ctypes.c_double, ci, i64, p, p, p, p, p, p]
+        lib.oracle_kv8_norm_rope.restype = None
+        lib.oracle_kv8_norm_rope.argtypes = [p, i64, i64, i64, p, p, i64, ci, p, ctypes.c_double, p]
         _lib = lib
     return _lib
 
@@ -379,3 +388,69 @@ def w8a8_mul_mat_sliced(wq: np.ndarray, wscale: np.ndarray, x: np.ndarray, with_
     d = np.concatenate([o[0] for o in outs], axis=0)
     c = np.concatenate([o[1] for o in outs], axis=0)
     return (d, c) if with_c else d
+
+
+class _KV8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ks", ctypes.c_void_p), ("vs", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("heads", ctypes.c_int64), ("P", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("blocks", ctypes.c_int64), ("lens", ctypes.c_void_p),
+                ("starts", ctypes.c_void_p), ("seqs", ctypes.c_int64)]
+
+
+class KV8:
+    """An int8 K/V cache and a batch of sequences over it, on the host: k int8
+    [pages][heads][P][D], v int8 [pages][heads][D][P], ks and vs F32
+    [pages][heads]; table int32 [seqs][blocks], lens [seqs], starts
+    [seqs + 1].  append changes the cache's arrays in place."""
+
+    def __init__(self, k, v, ks, vs, table, lens, starts):
+        self.k, self.v = np.ascontiguousarray(k, np.int8), np.ascontiguousarray(v, np.int8)
+        self.ks, self.vs = np.ascontiguousarray(ks, np.float32), np.ascontiguousarray(vs, np.float32)
+        self.table = np.ascontiguousarray(table, np.int32)
+        self.lens, self.starts = np.ascontiguousarray(lens, np.int32), np.ascontiguousarray(starts, np.int32)
+        self.pages, self.heads, self.P, self.D = self.k.shape
+        assert self.v.shape == (self.pages, self.heads, self.D, self.P)
+        assert (self.starts[1:] >= self.starts[:-1]).all() and len(self.starts) == len(self.lens) + 1 == len(self.table) + 1
+
+    def _struct(self):
+        return _KV8(_ptr(self.k), _ptr(self.v), _ptr(self.ks), _ptr(self.vs), self.pages, self.heads, self.P, self.D,
+                    _ptr(self.table), self.table.shape[1], _ptr(self.lens), _ptr(self.starts), len(self.lens))
+
+    def append(self, kx, vx):
+        kx, vx = np.ascontiguousarray(kx, np.float32), np.ascontiguousarray(vx, np.float32)
+        c = self._struct()
+        _load().oracle_kv8_append(ctypes.byref(c), _ptr(kx), _ptr(vx))
+
+    def read(self, rows):
+        """(k, v) F32 [rows][heads][D]; rows outside the batch's are NaN."""
+        kx = np.full((rows, self.heads, self.D), np.nan, np.float32)
+        vx = kx.copy()
+        c = self._struct()
+        _load().oracle_kv8_read(ctypes.byref(c), _ptr(kx), _ptr(vx))
+        return kx, vx
+
+    def attention(self, q, scale, causal=True, window=0):
+        """dict of float64 arrays: out, mag [rows][q_heads][D] (mag: the
+        probabilities' sum of |value|), lse, top (max |e|), spread (max of
+        |scale| k_scale sum|code| max|q|) [rows][q_heads]; rows outside the
+        batch's are NaN."""
+        q = np.ascontiguousarray(q, np.float32)
+        rows, heads, D = q.shape
+        r = {n: np.full((rows, heads, D) if n in ("out", "mag") else (rows, heads), np.nan)
+             for n in ("out", "mag", "lse", "top", "spread")}
+        e = np.zeros(max(1, int(self.lens.max(initial=0))))
+        c = self._struct()
+        _load().oracle_kv8_attention(ctypes.byref(c), _ptr(q), heads, float(scale), int(causal), int(window), _ptr(r["out"]),
+                                     _ptr(r["lse"]), _ptr(r["mag"]), _ptr(r["top"]), _ptr(r["spread"]), _ptr(e))
+        return r
+
+
+def kv8_norm_rope(x, pos, inv_freq, neighbours=False, weight=None, eps=1e-6):
+    """float64 [rows][heads][D] of F32 x, normed (with a weight) and rotated."""
+    x = np.ascontiguousarray(x, np.float32)
+    pos, inv_freq = np.ascontiguousarray(pos, np.int32), np.ascontiguousarray(inv_freq, np.float32)
+    weight = None if weight is None else np.ascontiguousarray(weight, np.float32)
+    y = np.empty(x.shape)
+    _load().oracle_kv8_norm_rope(_ptr(x), *x.shape, _ptr(pos), _ptr(inv_freq), len(inv_freq), int(neighbours),
+                                 None if weight is None else _ptr(weight), float(np.float32(eps)), _ptr(y))
+    return y

@@ -1,7 +1,7 @@
 /*
  * CPU oracle for the I2_S ternary-weight x int8-activation matmul (W2A8),
- * for the I8_S per-tensor int8 type with its fused mul_mat_add(_relu), and
- * for the per-channel W8A8 matmul.
+ * for the I8_S per-tensor int8 type with its fused mul_mat_add(_relu), for the
+ * per-channel W8A8 matmul, and for attention over an int8 K/V cache.
  *
  * TEST INFRASTRUCTURE ONLY.  This file is the plain, slow, obviously correct
  * definition that the GPU library is checked against.  Only the tests, the
@@ -411,4 +411,191 @@ int oracle_w8a8_mul_mat(const int8_t *w, const float *wscale, int64_t OC, int64_
     oracle_w8a8_matmul(a, as, M, w, wscale, OC, K, d, c);
     free(a); free(as);
     return 0;
+}
+
+/* ------------------------------------------------------------------------
+ * Attention over an int8 K/V cache (include/kv8.h states the layout and the
+ * formulas).  Codes and scales follow the quantization convention above
+ * (multiplier amax/127 floored at 1e-5, half away from zero) in binary32, one
+ * operation a step; rotation, norms and attention are binary64 throughout.
+ * Pins: tests/test_oracle_kv8_pins.py. */
+
+typedef struct {
+    int8_t *k, *v;         /* [pages][heads][P][D], [pages][heads][D][P] */
+    float *ks, *vs;        /* [pages][heads] */
+    int64_t pages, heads, P, D;
+    const int32_t *table;  /* [seqs][blocks] */
+    int64_t blocks;
+    const int32_t *lens, *starts;
+    int64_t seqs;
+} oracle_kv8;
+
+static int64_t oracle_kv8_page(const oracle_kv8 *c, int64_t b, int64_t t)
+{
+    int64_t j = t / c->P, p;
+    if (j >= c->blocks) return -1;
+    p = c->table[b * c->blocks + j];
+    return p >= 0 && p < c->pages ? p : -1;
+}
+
+static int8_t *oracle_kv8_code(const oracle_kv8 *c, int value, int64_t page, int64_t h, int64_t slot, int64_t d)
+{
+    int64_t base = (page * c->heads + h) * c->P * c->D;
+    return value ? c->v + base + d * c->P + slot : c->k + base + slot * c->D + d;
+}
+
+static int64_t oracle_kv8_len(const oracle_kv8 *c, int64_t b) { return c->lens[b] > 0 ? c->lens[b] : 0; }
+
+static int8_t oracle_kv8_round(float v)
+{
+    float r = roundf(v);
+    if (r > 127.0f) r = 127.0f;
+    if (r < -127.0f) r = -127.0f;
+    return (int8_t)r;
+}
+
+/* kx, vx: F32 [rows][heads][D]. */
+void oracle_kv8_append(const oracle_kv8 *c, const float *kx, const float *vx)
+{
+    for (int64_t b = 0; b < c->seqs; ++b) {
+        int64_t len = oracle_kv8_len(c, b), n = c->starts[b + 1] - c->starts[b], done = len - n;
+        for (int64_t j = 0; j * c->P < len; ++j) {
+            int64_t t0 = j * c->P, t1 = t0 + c->P < len ? t0 + c->P : len, page = oracle_kv8_page(c, b, t0);
+            if (t1 <= done || page < 0) continue;
+            for (int64_t h = 0; h < c->heads; ++h) {
+                for (int value = 0; value < 2; ++value) {
+                    const float *x = value ? vx : kx;
+                    float *scale = (value ? c->vs : c->ks) + page * c->heads + h;
+                    float amax = 0.0f, now;
+                    for (int64_t t = t0 > done ? t0 : done; t < t1; ++t)
+                        for (int64_t d = 0; d < c->D; ++d) {
+                            float a = fabsf(x[((c->starts[b] + t - done) * c->heads + h) * c->D + d]);
+                            if (a > amax) amax = a;
+                        }
+                    if (amax < 1e-5f) amax = 1e-5f;
+                    now = amax / 127.0f;
+                    if (t0 < done) {
+                        float before = *scale;
+                        if (now > before) {
+                            float ratio = before / now;
+                            for (int64_t t = t0; t < done; ++t)
+                                for (int64_t d = 0; d < c->D; ++d) {
+                                    int8_t *q = oracle_kv8_code(c, value, page, h, t - t0, d);
+                                    float moved = (float)*q * ratio;
+                                    *q = oracle_kv8_round(moved);
+                                }
+                        } else if (before >= now) {
+                            now = before;
+                        }
+                    }
+                    *scale = now;
+                    for (int64_t t = t0 > done ? t0 : done; t < t1; ++t)
+                        for (int64_t d = 0; d < c->D; ++d) {
+                            float v = x[((c->starts[b] + t - done) * c->heads + h) * c->D + d] / now;
+                            *oracle_kv8_code(c, value, page, h, t - t0, d) = oracle_kv8_round(v);
+                        }
+                }
+            }
+        }
+    }
+}
+
+/* kx, vx: F32 [rows][heads][D]; rows of the batch are written. */
+void oracle_kv8_read(const oracle_kv8 *c, float *kx, float *vx)
+{
+    for (int64_t b = 0; b < c->seqs; ++b) {
+        int64_t len = oracle_kv8_len(c, b), n = c->starts[b + 1] - c->starts[b];
+        for (int64_t i = 0; i < n; ++i) {
+            int64_t t = len - n + i, page = t < 0 ? -1 : oracle_kv8_page(c, b, t);
+            for (int64_t h = 0; h < c->heads; ++h)
+                for (int64_t d = 0; d < c->D; ++d) {
+                    int64_t o = ((c->starts[b] + i) * c->heads + h) * c->D + d;
+                    kx[o] = page < 0 ? 0.0f : (float)*oracle_kv8_code(c, 0, page, h, t % c->P, d) * c->ks[page * c->heads + h];
+                    vx[o] = page < 0 ? 0.0f : (float)*oracle_kv8_code(c, 1, page, h, t % c->P, d) * c->vs[page * c->heads + h];
+                }
+        }
+    }
+}
+
+/* q: F32 [rows][q_heads][D]; out double [rows][q_heads][D], lse double
+ * [rows][q_heads], and, for error bounds, mag double [rows][q_heads][D] = the
+ * probabilities' sum of |value|, and top double [rows][q_heads] = max |e| and
+ * spread double [rows][q_heads] = max over seen tokens of
+ * |scale| * k_scale * sum |code| * max|q|.  e: scratch of max length doubles. */
+void oracle_kv8_attention(const oracle_kv8 *c, const float *q, int64_t q_heads, double scale, int causal, int64_t window,
+                          double *out, double *lse, double *mag, double *top, double *spread, double *e)
+{
+    int64_t group = q_heads / c->heads;
+    for (int64_t b = 0; b < c->seqs; ++b) {
+        int64_t len = oracle_kv8_len(c, b), n = c->starts[b + 1] - c->starts[b];
+        for (int64_t i = 0; i < n; ++i) {
+            int64_t row = c->starts[b] + i, pos = len - n + i;
+            int64_t t0 = window > 0 && pos - window + 1 > 0 ? pos - window + 1 : 0;
+            int64_t t1 = causal && pos + 1 < len ? pos + 1 : len;
+            for (int64_t hq = 0; hq < q_heads; ++hq) {
+                int64_t h = hq / group, o = row * q_heads + hq;
+                const float *x = q + o * c->D;
+                double m = -INFINITY, l = 0.0, big = 0.0;
+                for (int64_t d = 0; d < c->D; ++d) {
+                    out[o * c->D + d] = mag[o * c->D + d] = 0.0;
+                    if (fabs((double)x[d]) > big) big = fabs((double)x[d]);
+                }
+                top[o] = spread[o] = 0.0;
+                for (int64_t t = t0; t < t1; ++t) {
+                    int64_t page = oracle_kv8_page(c, b, t);
+                    double dot = 0.0, codes = 0.0, ks;
+                    e[t] = -INFINITY;
+                    if (page < 0) continue;
+                    ks = c->ks[page * c->heads + h];
+                    for (int64_t d = 0; d < c->D; ++d) {
+                        double code = *oracle_kv8_code(c, 0, page, h, t % c->P, d);
+                        dot += (double)x[d] * code;
+                        codes += fabs(code);
+                    }
+                    e[t] = scale * (ks * dot);
+                    if (e[t] > m) m = e[t];
+                    if (fabs(e[t]) > top[o]) top[o] = fabs(e[t]);
+                    if (fabs(scale) * ks * codes * big > spread[o]) spread[o] = fabs(scale) * ks * codes * big;
+                }
+                for (int64_t t = t0; t < t1; ++t) {
+                    int64_t page = oracle_kv8_page(c, b, t);
+                    double p, vs;
+                    if (page < 0) continue;
+                    p = exp(e[t] - m);
+                    vs = c->vs[page * c->heads + h];
+                    l += p;
+                    for (int64_t d = 0; d < c->D; ++d) {
+                        double v = vs * *oracle_kv8_code(c, 1, page, h, t % c->P, d);
+                        out[o * c->D + d] += p * v;
+                        mag[o * c->D + d] += p * fabs(v);
+                    }
+                }
+                lse[o] = l > 0.0 ? m + log(l) : -INFINITY;
+                for (int64_t d = 0; d < c->D && l > 0.0; ++d) {
+                    out[o * c->D + d] /= l;
+                    mag[o * c->D + d] /= l;
+                }
+            }
+        }
+    }
+}
+
+/* x: F32 [rows][heads][D] -> y double of the same layout; weight NULL: no norm. */
+void oracle_kv8_norm_rope(const float *x, int64_t rows, int64_t heads, int64_t D, const int32_t *pos,
+                          const float *inv_freq, int64_t pairs, int neighbours, const float *weight, double eps, double *y)
+{
+    for (int64_t r = 0; r < rows; ++r)
+        for (int64_t h = 0; h < heads; ++h) {
+            const float *a = x + (r * heads + h) * D;
+            double *o = y + (r * heads + h) * D, ss = 0.0;
+            for (int64_t d = 0; d < D; ++d) ss += (double)a[d] * a[d];
+            for (int64_t d = 0; d < D; ++d) o[d] = weight ? a[d] / sqrt(ss / (double)D + eps) * weight[d] : a[d];
+            for (int64_t i = 0; i < pairs; ++i) {
+                double angle = (double)pos[r] * (double)inv_freq[i], cs = cos(angle), sn = sin(angle);
+                int64_t iu = neighbours ? 2 * i : i, iv = neighbours ? 2 * i + 1 : i + pairs;
+                double u = o[iu], v = o[iv];
+                o[iu] = u * cs - v * sn;
+                o[iv] = v * cs + u * sn;
+            }
+        }
 }

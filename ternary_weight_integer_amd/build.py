@@ -16,8 +16,8 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRCS = [os.path.join(PKG, "csrc", n) for n in ("i2s.hip", "i8s.hip", "noalloc.hip")]
-HEADERS = [os.path.join(ROOT, "include", h) for h in ("i2s.h", "i8s.h", "w8a8.h")]
+SRCS = [os.path.join(PKG, "csrc", n) for n in ("i2s.hip", "i8s.hip", "noalloc.hip", "kv8.hip")]
+HEADERS = [os.path.join(ROOT, "include", h) for h in ("i2s.h", "i8s.h", "w8a8.h", "kv8.h")]
 LIB = os.path.join(PKG, "libi2s.so")
 ARCH = "gfx950"
 
