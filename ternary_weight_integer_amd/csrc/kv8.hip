@@ -344,69 +344,444 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Cache c, Batch s, T *__r
 }
 
 // ---------------------------------------------------------------------------
-// Attention, the plain way: one wave per (row, query head), 64 tokens at a
-// time, sums in 64 bits.
+// Attention.
+//
+// A wave owns kRowTiles x 16 rows (row = query token and head of the K/V
+// head's group, so that a group shares what is read of the cache) and walks
+// tiles of 64 tokens.  Everything stays in registers, operands are loaded
+// straight into the order of the matrix instructions:
+//   S^T = K Q^T   int8 16x16x64.  The codes are exact, a query is held as
+//     kDigits signed base-256 digits of its row's largest magnitude (3 for
+//     F32 rows: 23 bits; 2 for 16-bit rows: 15 bits, of which their own
+//     mantissas fill 8 or 11), and the int32 dots are exact.
+//   O^T = V^T P^T  f16 16x16x32.  V's codes are exact in f16; a weight is one
+//     f16 (16-bit rows) or a sum of two (F32 rows: 22 bits).
+// The rows of K's four 16-token operands are taken from the tile in the order
+// 16 (m / 4) + 4 j + m % 4, which leaves lane (row, g) with the logits of the
+// 16 consecutive tokens 16 g ..: those are its k indices of P^T, and one
+// 16-byte load of a component's row in V is its part of V^T.  So probabilities
+// never leave their lane, and a lane's tokens lie in one page: its scales are
+// two scalars.
+//
+// The value scale is part of the weight: e = logit + log2(v_scale), running
+// maximum M over e, weight exp2(e - M + 15) (f16 then resolves weights down to
+// 2^-39 of the largest), and the denominator sums weight / v_scale.
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kNoMax = -1e30f;   // running maximum of a row that has seen nothing
+constexpr float kHeadroom = 15.0f; // weights are at most 2^15
+constexpr float kMinScale = 1e-30f;
+constexpr int kTile = 64;          // tokens
+
+struct Attend {
+  Cache c;
+  Batch s;
+  const void *q;
+  void *out;
+  float *lse, *acc, *ml;  // acc [splits][rows * q_heads][dim], ml [splits][rows * q_heads][2]
+  int64_t q_stride, out_stride, window;
+  float scale;  // times log2 e
+  int q_heads, group, causal, splits;
+};
+
+// What a tile of rows sees: tokens [begin, end), all of its rows [lo, hi), cut
+// into `used` parts of `part` token tiles.
+struct Range {
+  int begin, end, lo, hi, part, used;
+};
+
+constexpr int kMinPart = 4;  // token tiles of a part: shorter ones do not pay for joining
+
+__device__ inline int clamp_int(int64_t v, int top) { return v < 0 ? 0 : v < top ? static_cast<int>(v) : top; }
+
+__device__ inline Range range_of(const Attend &a, const Span &p, int first_row, int last_row) {
+  const int64_t ahead = static_cast<int64_t>(p.len) - p.n;
+  const int64_t p0 = ahead + first_row / a.group, p1 = ahead + last_row / a.group;
+  const int64_t held = static_cast<int64_t>(a.s.blocks) << a.c.lp;
+  const int top = held < p.len ? static_cast<int>(held) : p.len;
+  Range r;
+  r.hi = a.causal ? clamp_int(p0 + 1, top) : top;
+  r.end = a.causal ? clamp_int(p1 + 1, top) : top;
+  r.lo = a.window > 0 ? clamp_int(p1 - a.window + 1, top) : 0;
+  r.begin = (a.window > 0 ? clamp_int(p0 - a.window + 1, top) : 0) & ~(kTile - 1);
+  const int tiles = r.end > r.begin ? (r.end - r.begin + kTile - 1) / kTile : 0;
+  r.part = (tiles + a.splits - 1) / a.splits;
+  if (r.part < kMinPart) r.part = kMinPart;
+  r.used = (tiles + r.part - 1) / r.part;
+  return r;
+}
+
+// Max and sum over the four lanes that hold one row.
+__device__ inline float over_lanes_max(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ inline float over_lanes_sum(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// Four codes as f16: 0x6400 + u is 1024 + u for a byte u = code + 128.
+__device__ inline f16x4 codes_to_f16(int codes) {
+  const uint32_t u = static_cast<uint32_t>(codes) ^ 0x80808080u;
+  union {
+    uint32_t w[2];
+    f16x4 h;
+  } r;
+  r.w[0] = __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u);
+  r.w[1] = __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u);
+  return r.h - static_cast<f16>(1152.0f);
+}
 
 template <typename T>
-__global__ void __launch_bounds__(64) attention_kernel(Cache c, Batch s, const T *__restrict__ q, int64_t q_stride,
-                                                       int q_heads, float scale, int causal, int64_t window,
-                                                       T *__restrict__ out, int64_t out_stride, float *__restrict__ lse) {
-  __shared__ double x[KV8_MAX_DIM], w[64];
-  const int row = blockIdx.x, hq = blockIdx.y, lane = threadIdx.x;
-  int b;
-  if (s.starts) {
-    b = last_at_most(s.seqs, row, [&](int i) { return start_of(s, i); });
-    if (b < 0) return;
+__device__ inline void store4(T *p, f32x4 v) {
+  typedef T T4 __attribute__((ext_vector_type(4)));
+  T4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = static_cast<T>(v[i]);
+  *reinterpret_cast<T4 *>(p) = o;
+}
+
+// kChunks: 64-component chunks of a head (the head may end inside the last);
+// kTeam: the workgroup's 4 waves share the rows and take every fourth tile,
+// joined through shared memory; otherwise each has rows of its own.
+template <typename T, int kChunks, int kRowTiles, bool kTeam>
+__global__ void __launch_bounds__(kThreads) attention_kernel(Attend a) {
+  constexpr int kDigits = sizeof(T) == 4 ? 3 : 2;
+  constexpr int kParts = sizeof(T) == 4 ? 2 : 1;  // f16 parts of a weight
+  constexpr int kOut = 4 * kChunks;               // 16-component tiles
+  constexpr int kRows = 16 * kRowTiles;
+  constexpr int kBlockRows = kTeam ? kRows : 4 * kRows;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int n = lane & 15, g = lane >> 4;
+  const int h = blockIdx.y, split = blockIdx.z, G = a.group, D = a.c.dim, P = 1 << a.c.lp;
+
+  // Later rows see more: they are begun first.
+  const int x = gridDim.x - 1 - blockIdx.x;
+  int b, rel;
+  if (!a.s.starts) {
+    const int per = (a.s.per_seq * G + kBlockRows - 1) / kBlockRows;
+    b = x / per;
+    rel = x - b * per;
   } else {
-    b = row / s.per_seq;
+    auto key = [&](int i) { return start_of(a.s, i) * G / kBlockRows + i; };
+    b = last_at_most(a.s.seqs, x, key);
+    if (b < 0) return;
+    rel = x - key(b);
   }
-  const Span p = span_of(s, b);
-  if (row >= p.first + p.n) return;
-  const int D = c.dim, P = 1 << c.lp, h = hq / (q_heads / c.heads);
-  const int64_t pos = static_cast<int64_t>(p.len) - p.n + (row - p.first);
-  for (int d = lane; d < D; d += 64) x[d] = static_cast<float>(q[row * q_stride + hq * D + d]);
-  __syncthreads();
-  int64_t t1 = p.len, t0 = 0;
-  if (causal && pos + 1 < t1) t1 = pos + 1;
-  if (window > 0 && pos - window + 1 > 0) t0 = pos - window + 1;
-  double m = -HUGE_VAL, l = 0.0, acc[KV8_MAX_DIM / 64] = {};
-  for (int64_t base = t0; base < t1; base += 64) {
-    const int64_t t = base + lane;
-    double e = -HUGE_VAL, vs = 0.0;
-    if (t < t1) {
-      const int page = page_of(s, b, t >> c.lp, c.pages);
-      if (page >= 0) {
-        const int64_t at = static_cast<int64_t>(page) * c.heads + h;
-        const int8_t *k = c.k + at * P * D + (t & (P - 1)) * D;
-        double dot = 0.0;
-        for (int d = 0; d < D; ++d) dot += x[d] * k[d];
-        e = dot * c.k_scale[at] * scale;
-        vs = c.v_scale[at];
+  b = __builtin_amdgcn_readfirstlane(b);
+  rel = __builtin_amdgcn_readfirstlane(rel);
+  const Span p = span_of(a.s, b);
+  const int rows = p.n * G, row0 = rel * kBlockRows + (kTeam ? 0 : wave * kRows);
+  if (row0 >= rows) return;
+  const int last = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
+  const Range r = range_of(a, p, row0, last);
+  if (split >= (r.used > 1 ? r.used : 1)) return;
+  const int all = (r.end - r.begin + kTile - 1) / kTile, stop = (split + 1) * r.part;
+  const int end = stop < all ? r.begin + stop * kTile : r.end;
+
+  // Queries, as digits.
+  i32x4 q[kRowTiles][kChunks][kDigits];
+  float qs[kRowTiles];
+  int lo[kRowTiles], hi[kRowTiles];
+  int64_t at[kRowTiles];  // row * q_heads + head, or -1
+#pragma unroll
+  for (int t = 0; t < kRowTiles; ++t) {
+    const int row = row0 + 16 * t + n;
+    const bool live = row < rows;
+    const int i = live ? row / G : 0, hq = h * G + (live ? row - i * G : 0);
+    const int64_t pos = static_cast<int64_t>(p.len) - p.n + i;
+    at[t] = live ? static_cast<int64_t>(p.first + i) * a.q_heads + hq : -1;
+    hi[t] = !live ? 0 : a.causal ? clamp_int(pos + 1, r.end) : r.end;
+    lo[t] = a.window > 0 ? clamp_int(pos - a.window + 1, r.end) : 0;
+    const T *src = static_cast<const T *>(a.q) + (p.first + i) * a.q_stride + static_cast<int64_t>(hq) * D;
+    float v[kChunks][16];
+    float amax = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int d = 64 * c + 16 * g;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[c][k] = 0.0f;
+      if (live && d < D) {
+#pragma unroll
+        for (int k = 0; k < 16; k += Row<T>::kValues) load16(src + d + k, &v[c][k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 16; ++k) amax = fabsf(v[c][k]) < INFINITY ? fmaxf(amax, fabsf(v[c][k])) : INFINITY;
+    }
+    amax = over_lanes_max(amax);
+    constexpr float kTop = kDigits == 3 ? 127.0f * 65536.0f : 127.0f * 256.0f;
+    const float inv = amax > kMinScale && amax < INFINITY ? kTop / amax : 0.0f;
+    qs[t] = amax < INFINITY ? (amax > kMinScale ? amax / kTop * a.scale : 0.0f) : NAN;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t word[3] = {0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          int rest = static_cast<int>(rintf(v[c][4 * w + k] * inv));
+#pragma unroll
+          for (int z = kDigits - 1; z >= 0; --z) {
+            const int digit = static_cast<int8_t>(rest);
+            word[z] |= (static_cast<uint32_t>(digit) & 0xffu) << (8 * k);
+            rest = (rest - digit) >> 8;
+          }
+        }
+#pragma unroll
+        for (int z = 0; z < kDigits; ++z) q[t][c][z][w] = static_cast<int>(word[z]);
       }
     }
-    double top = e;
-    for (int k = 1; k < 64; k *= 2) top = fmax(top, __shfl_xor(top, k));
-    if (e != e) top = e;
-    top = fmax(top, m);
-    const double ref = top == -HUGE_VAL ? 0.0 : top, alpha = exp(m - ref), pr = exp(e - ref);
-    double sum = pr;
-    for (int k = 1; k < 64; k *= 2) sum += __shfl_xor(sum, k);
-    l = l * alpha + sum;
-    m = top;
-    w[lane] = pr * vs;
-    __syncthreads();
-    for (int i = 0, d = lane; d < D; d += 64, ++i) acc[i] *= alpha;
-    for (int k = 0; k < 64 && base + k < t1; ++k) {
-      const int page = page_of(s, b, (base + k) >> c.lp, c.pages);
-      if (page < 0) continue;
-      const int8_t *v = c.v + (static_cast<int64_t>(page) * c.heads + h) * P * D + ((base + k) & (P - 1));
-      for (int i = 0, d = lane; d < D; d += 64, ++i) acc[i] += w[k] * v[d * P];
-    }
-    __syncthreads();
   }
-  for (int i = 0, d = lane; d < D; d += 64, ++i)
-    out[row * out_stride + hq * D + d] = static_cast<T>(static_cast<float>(l == 0.0 ? 0.0 : acc[i] / l));
-  if (lse && lane == 0) lse[static_cast<int64_t>(row) * q_heads + hq] = static_cast<float>(l == 0.0 ? -HUGE_VAL : m + log(l));
+
+  f32x4 acc[kRowTiles][kOut] = {};
+  float m[kRowTiles], l[kRowTiles];  // m: the running maximum less kHeadroom
+#pragma unroll
+  for (int t = 0; t < kRowTiles; ++t) {
+    m[t] = kNoMax;
+    l[t] = 0.0f;
+  }
+
+  const int64_t page_bytes = static_cast<int64_t>(a.c.heads) * P * D;
+  const int8_t *kbase = a.c.k + static_cast<int64_t>(h) * P * D, *vbase = a.c.v + static_cast<int64_t>(h) * P * D;
+  const int step = kTeam ? 4 * kTile : kTile;
+  auto page_at = [&](int t) { return t < r.end ? page_of(a.s, b, t >> a.c.lp, a.c.pages) : -1; };
+  int t0 = r.begin + split * r.part * kTile + (kTeam ? wave * kTile : 0);
+  int kpage = -1, vpage = -1;
+  if (t0 < end) {
+    kpage = page_at(t0 + 16 * (n >> 2));
+    vpage = page_at(t0 + 16 * g);
+  }
+  for (; t0 < end; t0 += step) {
+    // Holes load page 0 in their place; their weights are zero.
+    const bool hole = vpage < 0;
+    const int64_t kp = kpage < 0 ? 0 : kpage, vp = hole ? 0 : vpage;
+    const float ks = hole ? 0.0f : a.c.k_scale[vp * a.c.heads + h];
+    const float vs = hole ? 1.0f : fmaxf(a.c.v_scale[vp * a.c.heads + h], kMinScale);
+    const int kslot = ((t0 + 16 * (n >> 2)) & (P - 1)) + (n & 3);
+    const int8_t *kptr = kbase + kp * page_bytes + kslot * D + 16 * g;
+    const int8_t *vptr = vbase + vp * page_bytes + n * P + ((t0 + 16 * g) & (P - 1));
+    i32x4 kc[4][kChunks], vc[kOut];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        kc[j][c] = i32x4{0, 0, 0, 0};
+        if (64 * c + 16 * g < D) kc[j][c] = *reinterpret_cast<const i32x4 *>(kptr + 4 * j * D + 64 * c);
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < kOut; ++d) {
+      vc[d] = i32x4{0, 0, 0, 0};
+      if (16 * d < D) vc[d] = *reinterpret_cast<const i32x4 *>(vptr + 16 * d * P);
+    }
+    if (t0 + step < end) {
+      kpage = page_at(t0 + step + 16 * (n >> 2));
+      vpage = page_at(t0 + step + 16 * g);
+    }
+    const float lvs = hole ? -INFINITY : __log2f(vs), rvs = 1.0f / vs;
+    const bool edge = t0 < r.lo || t0 + kTile > r.hi;
+
+    union Weights {
+      f16x2 pair[8];
+      f16x8 half[2];
+    } w[kRowTiles][kParts];
+#pragma unroll
+    for (int t = 0; t < kRowTiles; ++t) {
+      float f[16];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        i32x4 dot[kDigits];
+#pragma unroll
+        for (int z = 0; z < kDigits; ++z) {
+          dot[z] = i32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            dot[z] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kc[j][c], q[t][c][z], dot[z], 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (kDigits == 3) {
+            f[4 * j + i] = fmaf(static_cast<float>(dot[0][i]), 65536.0f, static_cast<float>(dot[1][i] * 256 + dot[2][i]));
+          } else {
+            f[4 * j + i] = static_cast<float>(dot[0][i] * 256 + dot[1][i]);
+          }
+        }
+      }
+      const float ck = qs[t] * ks;
+      float e[16];
+      auto exponents = [&](float base) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) e[k] = fmaf(f[k], ck, base);
+        if (edge) {
+          const int under = lo[t] - (t0 + 16 * g), over = hi[t] - (t0 + 16 * g);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) e[k] = k >= under && k < over ? e[k] : -INFINITY;
+        }
+        float top = e[0];
+#pragma unroll
+        for (int k = 1; k < 16; ++k) top = fmaxf(top, e[k]);
+        return top;
+      };
+      float top = exponents(lvs - m[t]);
+      if (__any(top > kHeadroom)) {
+        top = over_lanes_max(exponents(lvs)) - kHeadroom;
+        const float now = fmaxf(m[t], top), shrink = __builtin_amdgcn_exp2f(m[t] - now);
+        m[t] = now;
+        l[t] *= shrink;
+#pragma unroll
+        for (int d = 0; d < kOut; ++d) acc[t][d] *= shrink;
+        exponents(lvs - now);
+      }
+      float sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 16; k += 2) {
+        const float p0 = __builtin_amdgcn_exp2f(e[k]), p1 = __builtin_amdgcn_exp2f(e[k + 1]);
+        sum += p0 + p1;
+        const f16x2 near = {static_cast<f16>(p0), static_cast<f16>(p1)};
+        w[t][0].pair[k / 2] = near;
+        if (kParts == 2)
+          w[t][kParts - 1].pair[k / 2] = f16x2{static_cast<f16>(p0 - static_cast<float>(near[0])),
+                                               static_cast<f16>(p1 - static_cast<float>(near[1]))};
+      }
+      l[t] = fmaf(sum, rvs, l[t]);
+    }
+#pragma unroll
+    for (int d = 0; d < kOut; ++d) {
+      if (16 * d >= D) continue;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        union {
+          f16x4 part[2];
+          f16x8 all;
+        } v;
+        v.part[0] = codes_to_f16(vc[d][2 * k]);
+        v.part[1] = codes_to_f16(vc[d][2 * k + 1]);
+#pragma unroll
+        for (int t = 0; t < kRowTiles; ++t) {
+#pragma unroll
+          for (int z = 0; z < kParts; ++z)
+            acc[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v.all, w[t][z].half[k], acc[t][d], 0, 0, 0);
+        }
+      }
+    }
+  }
+
+  // The lanes' sums, then (a team) the waves' results.
+#pragma unroll
+  for (int t = 0; t < kRowTiles; ++t) l[t] = over_lanes_sum(l[t]);
+  auto finish = [&](int t, int d, f32x4 o) {
+    if (at[t] < 0 || 16 * d >= D) return;
+    const int c = 16 * d + 4 * g;
+    if (r.used > 1) {
+      const int64_t row = static_cast<int64_t>(split) * a.s.rows * a.q_heads + at[t];
+      *reinterpret_cast<f32x4 *>(a.acc + row * D + c) = o;
+      if (d == 0 && g == 0) {
+        a.ml[2 * row] = m[t];
+        a.ml[2 * row + 1] = l[t];
+      }
+    } else {
+      const float inv = l[t] == 0.0f ? 0.0f : 1.0f / l[t];
+      const int64_t row = at[t] / a.q_heads, hq = at[t] - row * a.q_heads;
+      store4(static_cast<T *>(a.out) + row * a.out_stride + hq * D + c, o * inv);
+      if (d == 0 && g == 0 && a.lse) a.lse[at[t]] = l[t] == 0.0f ? -INFINITY : 0.69314718055994531f * (m[t] + log2f(l[t]));
+    }
+  };
+  if constexpr (kTeam) {
+    __shared__ f32x4 parts[4][kOut][64];
+    __shared__ float stats[4][16][2];
+#pragma unroll
+    for (int t = 0; t < kRowTiles; ++t) {
+      if (t > 0) __syncthreads();
+      if (g == 0) {
+        stats[wave][n][0] = m[t];
+        stats[wave][n][1] = l[t];
+      }
+#pragma unroll
+      for (int d = 0; d < kOut; ++d) parts[wave][d][lane] = acc[t][d];
+      __syncthreads();
+      float wm[4], wl[4], now = kNoMax;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        wm[k] = stats[k][n][0];
+        wl[k] = stats[k][n][1];
+        now = fmaxf(now, wm[k]);
+      }
+      l[t] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        wm[k] = __builtin_amdgcn_exp2f(wm[k] - now);
+        l[t] = fmaf(wm[k], wl[k], l[t]);
+      }
+      m[t] = now;
+#pragma unroll
+      for (int d = 0; d < kOut; ++d) {
+        if ((d & 3) != wave) continue;
+        f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o += wm[k] * parts[k][d][lane];
+        finish(t, d, o);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < kRowTiles; ++t) {
+#pragma unroll
+      for (int d = 0; d < kOut; ++d) finish(t, d, acc[t][d]);
+    }
+  }
+}
+
+// Joins the parts of rows that were split: one workgroup per row and head,
+// waves over parts, lanes over components.  unit: rows of the attention's tile.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) join_kernel(Attend a, int unit) {
+  __shared__ float sums[4][KV8_MAX_DIM], sl[4];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int row = blockIdx.x, hq = blockIdx.y, D = a.c.dim;
+  int b;
+  if (a.s.starts) {
+    b = last_at_most(a.s.seqs, row, [&](int i) { return start_of(a.s, i); });
+    if (b < 0) return;
+  } else {
+    b = row / a.s.per_seq;
+  }
+  const Span p = span_of(a.s, b);
+  if (row >= p.first + p.n) return;
+  const int in_group = (row - p.first) * a.group + hq % a.group, row0 = in_group / unit * unit;
+  const int rows = p.n * a.group;
+  const Range r = range_of(a, p, row0, (row0 + unit < rows ? row0 + unit : rows) - 1);
+  if (r.used <= 1) return;
+  const int64_t each = static_cast<int64_t>(a.s.rows) * a.q_heads, at = static_cast<int64_t>(row) * a.q_heads + hq;
+  float now = kNoMax;
+  for (int k = lane; k < r.used; k += 64) now = fmaxf(now, a.ml[2 * (k * each + at)]);
+  now = wave_max(now);
+  float l = 0.0f, o[KV8_MAX_DIM / 64] = {};
+  for (int k = wave; k < r.used; k += 4) {
+    const int64_t from = k * each + at;
+    const float w = __builtin_amdgcn_exp2f(a.ml[2 * from] - now);
+    l = fmaf(w, a.ml[2 * from + 1], l);
+#pragma unroll
+    for (int i = 0; i < KV8_MAX_DIM / 64; ++i)
+      if (lane + 64 * i < D) o[i] = fmaf(w, a.acc[from * D + lane + 64 * i], o[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < KV8_MAX_DIM / 64; ++i) sums[wave][lane + 64 * i] = o[i];
+  if (lane == 0) sl[wave] = l;
+  __syncthreads();
+  l = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  for (int d = threadIdx.x; d < D; d += kThreads)
+    static_cast<T *>(a.out)[row * a.out_stride + static_cast<int64_t>(hq) * D + d] =
+        static_cast<T>(((sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d])) * inv);
+  if (a.lse && threadIdx.x == 0) a.lse[at] = l == 0.0f ? -INFINITY : 0.69314718055994531f * (now + log2f(l));
 }
 
 // ---------------------------------------------------------------------------
@@ -557,6 +932,60 @@ inline int64_t slots(const Batch &s, int lp) {
   return static_cast<int64_t>(s.seqs) * (((s.per_seq + (INT64_C(1) << lp) - 2) >> lp) + 1);
 }
 
+// How an attention call is laid out: rows of a wave, whether a workgroup's
+// waves share them, and into how many parts the tokens are cut.
+struct Plan {
+  int row_tiles, splits;
+  bool team;
+  int64_t blocks;  // workgroups along the rows
+};
+
+Plan plan_of(const Cache &c, const Batch &s, int64_t max_len, int64_t q_heads) {
+  const int64_t group = q_heads / c.heads, rows = s.rows * group / s.seqs;  // of a sequence, on average
+  Plan p;
+  p.team = rows <= 64;
+  p.row_tiles = rows <= 16 || c.dim > 128 ? 1 : 2;
+  const int64_t unit = 16 * p.row_tiles * (p.team ? 1 : 4);
+  p.blocks = s.starts ? s.rows * group / unit + s.seqs : (s.per_seq * group + unit - 1) / unit * s.seqs;
+  const int64_t held = static_cast<int64_t>(s.blocks) << c.lp;
+  if (max_len <= 0 || max_len > held) max_len = held;
+  const int64_t most = (max_len + kTile * kMinPart - 1) / (kTile * kMinPart);
+  int64_t splits = 1024 / (p.blocks * c.heads);
+  if (splits > most) splits = most;
+  if (splits > 1024) splits = 1024;
+  p.splits = splits < 1 ? 1 : static_cast<int>(splits);
+  return p;
+}
+
+// Checks shared by kv8_attention and its workspace's size.
+int check_attention(const kv8_cache *cache, const kv8_batch *batch, int type, int64_t q_heads, int64_t rows, Cache &c,
+                    Batch &s) {
+  if (const int st = check_batch(cache, batch, type, rows, c, s)) return st;
+  if (q_heads < 1 || q_heads % c.heads) return I2S_EINVAL;
+  if (q_heads > 65535 || rows * (q_heads / c.heads) > kMaxRows ||
+      (static_cast<int64_t>(s.blocks) << c.lp) > kMaxRows - 4 * KV8_MAX_PAGE)
+    return I2S_ERANGE;
+  return I2S_OK;
+}
+
+inline size_t workspace_of(const Plan &p, const Cache &c, const Batch &s, int64_t q_heads) {
+  return p.splits > 1 ? static_cast<size_t>(p.splits) * s.rows * q_heads * (c.dim + 2) * sizeof(float) : 0;
+}
+
+template <typename T, int kChunks>
+int launch_attention(const Plan &p, const Attend &a, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(p.blocks), a.c.heads, p.splits);
+  constexpr int kMost = kChunks > 2 ? 1 : 2;  // row tiles that fit the registers
+  if (p.team && p.row_tiles == 1) {
+    attention_kernel<T, kChunks, 1, true><<<grid, kThreads, 0, stream>>>(a);
+  } else if (p.team) {
+    attention_kernel<T, kChunks, kMost, true><<<grid, kThreads, 0, stream>>>(a);
+  } else {
+    attention_kernel<T, kChunks, kMost, false><<<grid, kThreads, 0, stream>>>(a);
+  }
+  return hip_status();
+}
+
 template <typename F>
 int by_type(int type, F f) {
   if (type == KV8_F32) return f(float());
@@ -607,31 +1036,46 @@ extern "C" size_t kv8_attention_workspace_bytes(const kv8_cache *cache, const kv
                                                 int64_t rows) {
   Cache c;
   Batch s;
-  if (check_batch(cache, batch, KV8_F32, rows, c, s) || q_heads < 1 || q_heads % c.heads) return 0;
-  return 0;
+  if (check_attention(cache, batch, KV8_F32, q_heads, rows, c, s) || rows == 0 || s.seqs == 0) return 0;
+  return workspace_of(plan_of(c, s, batch->max_len, q_heads), c, s, q_heads);
 }
 
 extern "C" int kv8_attention(const kv8_cache *cache, const kv8_batch *batch, int type, const void *q, int64_t q_stride,
                              int64_t q_heads, int64_t rows, float scale, int causal, int64_t window, void *out,
                              int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
-  Cache c;
-  Batch s;
-  if (const int st = check_batch(cache, batch, type, rows, c, s)) return st;
-  if (q_heads < 1 || q_heads % c.heads || window < 0 || !(fabsf(scale) < INFINITY)) return I2S_EINVAL;
-  if (q_heads > 65535) return I2S_ERANGE;
-  if (rows == 0 || s.seqs == 0) return I2S_OK;
-  const int64_t width = q_heads * c.dim;
+  Attend a;
+  if (const int st = check_attention(cache, batch, type, q_heads, rows, a.c, a.s)) return st;
+  if (window < 0 || !(fabsf(scale) < INFINITY)) return I2S_EINVAL;
+  if (rows == 0 || a.s.seqs == 0) return I2S_OK;
+  const int64_t width = q_heads * a.c.dim;
   if (bad_rows(q, q_stride, width, value_bytes(type)) || bad_rows(out, out_stride, width, value_bytes(type)) ||
       !aligned(lse, 4))
     return I2S_EINVAL;
-  const size_t need = kv8_attention_workspace_bytes(cache, batch, q_heads, rows);
+  const Plan p = plan_of(a.c, a.s, batch->max_len, q_heads);
+  if (p.blocks > 0x7fffffff) return I2S_ERANGE;
+  const size_t need = workspace_of(p, a.c, a.s, q_heads);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return I2S_EWORKSPACE;
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.acc = static_cast<float *>(workspace);
+  a.ml = need ? a.acc + static_cast<int64_t>(p.splits) * rows * q_heads * a.c.dim : nullptr;
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.window = window;
+  a.scale = scale * 1.44269504088896341f;
+  a.q_heads = static_cast<int>(q_heads);
+  a.group = static_cast<int>(q_heads / a.c.heads);
+  a.causal = causal != 0;
+  a.splits = p.splits;
+  const hipStream_t on = static_cast<hipStream_t>(stream);
   return by_type(type, [&](auto t) {
     typedef decltype(t) T;
-    attention_kernel<T><<<dim3(static_cast<unsigned>(rows), static_cast<unsigned>(q_heads)), 64, 0,
-                          static_cast<hipStream_t>(stream)>>>(c, s, static_cast<const T *>(q), q_stride,
-                                                              static_cast<int>(q_heads), scale, causal, window,
-                                                              static_cast<T *>(out), out_stride, lse);
+    const int st = a.c.dim <= 64    ? launch_attention<T, 1>(p, a, on)
+                   : a.c.dim <= 128 ? launch_attention<T, 2>(p, a, on)
+                                    : launch_attention<T, 4>(p, a, on);
+    if (st || p.splits == 1) return st;
+    join_kernel<T><<<dim3(static_cast<unsigned>(rows), a.q_heads), kThreads, 0, on>>>(a, 16 * p.row_tiles);
     return hip_status();
   });
 }
