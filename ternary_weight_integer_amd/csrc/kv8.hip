@@ -13,6 +13,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kv8.h"
 
 namespace {
@@ -24,6 +26,7 @@ constexpr int64_t kMaxRows = 0x7fffffff;
 
 typedef _Float16 f16;
 typedef __bf16 bf16;
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
@@ -109,21 +112,41 @@ __device__ inline Span span_of(const Batch &s, int b) {
   return p;
 }
 
-// The last sequence whose key(b) is at most x (-1: none), for a rising key,
-// found 64 candidates at a time by the wave; every lane gets it.
+// The sequence that holds place x of a grid: the last whose key(b, start(b))
+// is at most x, for a rising key (b = -1: none).  Up to 63 sequences are
+// looked at in one load of starts and lengths, whose latency is all that a
+// workgroup then waits for; more are searched 64 candidates at a time.
 template <typename Key>
-__device__ inline int last_at_most(int seqs, int x, Key key) {
+__device__ inline Span find(const Batch &s, int x, Key key) {
   const int lane = threadIdx.x & 63;
-  int lo = 0, hi = seqs;
+  if (s.seqs < 64) {
+    const int v = start_of(s, lane < s.seqs ? lane : s.seqs);
+    const int len = s.lens[lane < s.seqs ? lane : 0];
+    const int count = __popcll(__ballot(lane < s.seqs && key(lane, v) <= x));
+    Span p;
+    p.b = count - 1;
+    const int b = count > 0 ? count - 1 : 0;
+    p.first = __builtin_amdgcn_readlane(v, b);
+    const int n = __builtin_amdgcn_readlane(v, b + 1) - p.first, l = __builtin_amdgcn_readlane(len, b);
+    p.n = n > 0 ? n : 0;
+    p.len = l > 0 ? l : 0;
+    return p;
+  }
+  int lo = 0, hi = s.seqs;
   while (true) {
     const int step = (hi - lo + 63) >> 6;
     const int64_t i = lo + static_cast<int64_t>(lane) * step;
-    const int count = __popcll(__ballot(i < hi && key(static_cast<int>(i < hi ? i : lo)) <= x));
-    if (count == 0) return -1;
+    const int at = static_cast<int>(i < hi ? i : lo);
+    const int count = __popcll(__ballot(i < hi && key(at, start_of(s, at)) <= x));
+    if (count == 0) {
+      Span p = {-1, 0, 0, 0};
+      return p;
+    }
     lo += (count - 1) * step;
     hi = hi < lo + step ? hi : lo + step;
-    if (step == 1) return lo;
+    if (step == 1) break;
   }
+  return span_of(s, __builtin_amdgcn_readfirstlane(lo));
 }
 
 // Page of block j of sequence b, or -1 for a hole.
@@ -138,18 +161,18 @@ __device__ inline int page_of(const Batch &s, int b, int64_t j, int pages) {
 // sequences are distinct and rows / P + 2 seqs of them suffice, whatever the
 // device's starts say.
 __device__ inline bool slot_of(const Batch &s, int lp, int x, Span &p, int64_t &j) {
-  int b, rel;
+  int rel;
   if (!s.starts) {
-    const int per = ((s.per_seq + (1 << lp) - 2) >> lp) + 1;
-    b = x / per;
+    const int per = ((s.per_seq + (1 << lp) - 2) >> lp) + 1, b = x / per;
     rel = x - b * per;
     if (b >= s.seqs) return false;
+    p = span_of(s, b);
   } else {
-    b = last_at_most(s.seqs, x, [&](int i) { return (start_of(s, i) >> lp) + 2 * i; });
-    if (b < 0) return false;
-    rel = x - ((start_of(s, b) >> lp) + 2 * b);
+    auto key = [&](int i, int start) { return (start >> lp) + 2 * i; };
+    p = find(s, x, key);
+    if (p.b < 0) return false;
+    rel = x - key(p.b, p.first);
   }
-  p = span_of(s, b);
   const int done = p.len - p.n;
   j = static_cast<int64_t>((done > 0 ? done : 0) >> lp) + rel;
   return true;
@@ -346,16 +369,17 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Cache c, Batch s, T *__r
 // ---------------------------------------------------------------------------
 // Attention.
 //
-// A wave owns kRowTiles x 16 rows (row = query token and head of the K/V
+// A wave owns one or two tiles of 16 rows (row = query token and head of the K/V
 // head's group, so that a group shares what is read of the cache) and walks
 // tiles of 64 tokens.  Everything stays in registers, operands are loaded
 // straight into the order of the matrix instructions:
 //   S^T = K Q^T   int8 16x16x64.  The codes are exact, a query is held as
-//     kDigits signed base-256 digits of its row's largest magnitude (3 for
-//     F32 rows: 23 bits; 2 for 16-bit rows: 15 bits, of which their own
-//     mantissas fill 8 or 11), and the int32 dots are exact.
+//     kDigits signed base-256 digits of its row's largest magnitude (3, 23
+//     bits, for F32 and F16 rows; 2, 15 bits, for BF16 rows, whose mantissas
+//     have 8), and the int32 dots are exact.
 //   O^T = V^T P^T  f16 16x16x32.  V's codes are exact in f16; a weight is one
-//     f16 (16-bit rows) or a sum of two (F32 rows: 22 bits).
+//     f16 (BF16 rows) or a sum of two (22 bits).  With one, and 2 digits, an
+//     F16 result's error was 1.3 times its own rounding.
 // The rows of K's four 16-token operands are taken from the tile in the order
 // 16 (m / 4) + 4 j + m % 4, which leaves lane (row, g) with the logits of the
 // 16 consecutive tokens 16 g ..: those are its k indices of P^T, and one
@@ -375,6 +399,9 @@ constexpr float kNoMax = -1e30f;   // running maximum of a row that has seen not
 constexpr float kHeadroom = 15.0f; // weights are at most 2^15
 constexpr float kMinScale = 1e-30f;
 constexpr int kTile = 64;          // tokens
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr int kMaxSplits = 256;
+constexpr int kUnits = 256;        // compute units
 
 struct Attend {
   Cache c;
@@ -385,7 +412,21 @@ struct Attend {
   int64_t q_stride, out_stride, window;
   float scale;  // times log2 e
   int q_heads, group, causal, splits;
+  int blocks, round;  // workgroups along the rows of one head and part, and those that fill the compute units once
 };
+
+// x less the kHalf-th of a pair of f16, exact where that is x rounded: one
+// mixed-precision operation (the compiler takes two).
+template <int kHalf>
+__device__ inline float less(float x, f16x2 pair) {
+  float r;
+  if (kHalf == 0) {
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[0,0,0] op_sel_hi:[1,0,0]" : "=v"(r) : "v"(pair), "v"(x));
+  } else {
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r) : "v"(pair), "v"(x));
+  }
+  return r;
+}
 
 // What a tile of rows sees: tokens [begin, end), all of its rows [lo, hi), cut
 // into `used` parts of `part` token tiles.
@@ -393,7 +434,7 @@ struct Range {
   int begin, end, lo, hi, part, used;
 };
 
-constexpr int kMinPart = 4;  // token tiles of a part: shorter ones do not pay for joining
+constexpr int kMinPart = 8;  // token tiles of a part: shorter ones do not pay for joining
 
 __device__ inline int clamp_int(int64_t v, int top) { return v < 0 ? 0 : v < top ? static_cast<int>(v) : top; }
 
@@ -449,339 +490,631 @@ __device__ inline void store4(T *p, f32x4 v) {
   *reinterpret_cast<T4 *>(p) = o;
 }
 
-// kChunks: 64-component chunks of a head (the head may end inside the last);
-// kTeam: the workgroup's 4 waves share the rows and take every fourth tile,
-// joined through shared memory; otherwise each has rows of its own.
-template <typename T, int kChunks, int kRowTiles, bool kTeam>
-__global__ void __launch_bounds__(kThreads) attention_kernel(Attend a) {
-  constexpr int kDigits = sizeof(T) == 4 ? 3 : 2;
-  constexpr int kParts = sizeof(T) == 4 ? 2 : 1;  // f16 parts of a weight
-  constexpr int kOut = 4 * kChunks;               // 16-component tiles
-  constexpr int kRows = 16 * kRowTiles;
-  constexpr int kBlockRows = kTeam ? kRows : 4 * kRows;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int n = lane & 15, g = lane >> 4;
-  const int h = blockIdx.y, split = blockIdx.z, G = a.group, D = a.c.dim, P = 1 << a.c.lp;
+// The sequence, rows, head and part of a workgroup.  Heads are dealt first:
+// workgroups go to the 8 dies in turn, so that a die's cache holds few heads.
+// Later rows see more (causal), so they are begun first, and every other round
+// of workgroups over the compute units runs backwards: units that share one
+// then have about the same to do between them.
+struct Place {
+  Span p;
+  int rows, row0;  // rows of the sequence, first row of the workgroup
+  int h, split;
+};
 
-  // Later rows see more: they are begun first.
-  const int x = gridDim.x - 1 - blockIdx.x;
-  int b, rel;
+__device__ inline bool place_of(const Attend &a, int block_rows, Place &w) {
+  const int rest = blockIdx.x / a.c.heads, G = a.group;
+  w.h = blockIdx.x - rest * a.c.heads;
+  int x = rest / a.splits;
+  w.split = rest - x * a.splits;
+  const int turn = x / a.round;
+  if ((turn & 1) && (turn + 1) * a.round <= a.blocks) x = (2 * turn + 1) * a.round - 1 - x;
+  x = a.blocks - 1 - x;
+  int rel;
   if (!a.s.starts) {
-    const int per = (a.s.per_seq * G + kBlockRows - 1) / kBlockRows;
-    b = x / per;
+    const int per = (a.s.per_seq * G + block_rows - 1) / block_rows, b = x / per;
     rel = x - b * per;
+    w.p = span_of(a.s, b);
   } else {
-    auto key = [&](int i) { return start_of(a.s, i) * G / kBlockRows + i; };
-    b = last_at_most(a.s.seqs, x, key);
-    if (b < 0) return;
-    rel = x - key(b);
+    auto key = [&](int i, int start) { return start * G / block_rows + i; };
+    w.p = find(a.s, x, key);
+    if (w.p.b < 0) return false;
+    rel = x - key(w.p.b, w.p.first);
   }
-  b = __builtin_amdgcn_readfirstlane(b);
-  rel = __builtin_amdgcn_readfirstlane(rel);
-  const Span p = span_of(a.s, b);
-  const int rows = p.n * G, row0 = rel * kBlockRows + (kTeam ? 0 : wave * kRows);
-  if (row0 >= rows) return;
-  const int last = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
-  const Range r = range_of(a, p, row0, last);
-  if (split >= (r.used > 1 ? r.used : 1)) return;
+  w.rows = w.p.n * G;
+  w.row0 = rel * block_rows;
+  return w.row0 < w.rows;
+}
+
+// Tokens [begin, end) of a part.
+struct Part {
+  int begin, end;
+};
+
+__device__ inline Part part_of(const Range &r, int split) {
   const int all = (r.end - r.begin + kTile - 1) / kTile, stop = (split + 1) * r.part;
-  const int end = stop < all ? r.begin + stop * kTile : r.end;
+  return {r.begin + split * r.part * kTile, stop < all ? r.begin + stop * kTile : r.end};
+}
 
-  // Queries, as digits.
-  i32x4 q[kRowTiles][kChunks][kDigits];
-  float qs[kRowTiles];
-  int lo[kRowTiles], hi[kRowTiles];
-  int64_t at[kRowTiles];  // row * q_heads + head, or -1
-#pragma unroll
-  for (int t = 0; t < kRowTiles; ++t) {
-    const int row = row0 + 16 * t + n;
-    const bool live = row < rows;
-    const int i = live ? row / G : 0, hq = h * G + (live ? row - i * G : 0);
-    const int64_t pos = static_cast<int64_t>(p.len) - p.n + i;
-    at[t] = live ? static_cast<int64_t>(p.first + i) * a.q_heads + hq : -1;
-    hi[t] = !live ? 0 : a.causal ? clamp_int(pos + 1, r.end) : r.end;
-    lo[t] = a.window > 0 ? clamp_int(pos - a.window + 1, r.end) : 0;
-    const T *src = static_cast<const T *>(a.q) + (p.first + i) * a.q_stride + static_cast<int64_t>(hq) * D;
-    float v[kChunks][16];
-    float amax = 0.0f;
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int d = 64 * c + 16 * g;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) v[c][k] = 0.0f;
-      if (live && d < D) {
-#pragma unroll
-        for (int k = 0; k < 16; k += Row<T>::kValues) load16(src + d + k, &v[c][k]);
-      }
-#pragma unroll
-      for (int k = 0; k < 16; ++k) amax = fabsf(v[c][k]) < INFINITY ? fmaxf(amax, fabsf(v[c][k])) : INFINITY;
-    }
-    amax = over_lanes_max(amax);
-    constexpr float kTop = kDigits == 3 ? 127.0f * 65536.0f : 127.0f * 256.0f;
-    const float inv = amax > kMinScale && amax < INFINITY ? kTop / amax : 0.0f;
-    qs[t] = amax < INFINITY ? (amax > kMinScale ? amax / kTop * a.scale : 0.0f) : NAN;
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t word[3] = {0, 0, 0};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          int rest = static_cast<int>(rintf(v[c][4 * w + k] * inv));
-#pragma unroll
-          for (int z = kDigits - 1; z >= 0; --z) {
-            const int digit = static_cast<int8_t>(rest);
-            word[z] |= (static_cast<uint32_t>(digit) & 0xffu) << (8 * k);
-            rest = (rest - digit) >> 8;
-          }
-        }
-#pragma unroll
-        for (int z = 0; z < kDigits; ++z) q[t][c][z][w] = static_cast<int>(word[z]);
-      }
-    }
+// Pages of a tile's tokens.  Loads are never conditional: the counters by
+// which a wave waits for them could not tell how many are on their way.  Past
+// the last tile its tokens are loaded again, holes load page 0 in their place
+// (their weights are zero).
+struct Pages {
+  const int32_t *table;
+  const int8_t *k, *v;
+  const float *k_scale, *v_scale;
+  int64_t bytes;  // of a page
+  int heads, pages, lp, last;
+
+  __device__ Pages(const Attend &a, int b, int h, int D, int end)
+      : table(a.s.table + b * a.s.table_stride), heads(a.c.heads), pages(a.c.pages), lp(a.c.lp), last(end - 1) {
+    const int64_t head = static_cast<int64_t>(D) << lp;
+    bytes = heads * head;
+    k = a.c.k + h * head;
+    v = a.c.v + h * head;
+    k_scale = a.c.k_scale + h;
+    v_scale = a.c.v_scale + h;
   }
+  __device__ int entry(int t) const { return table[(t < last ? t : last) >> lp]; }
+  __device__ bool hole(int entry) const { return static_cast<unsigned>(entry) >= static_cast<unsigned>(pages); }
+  __device__ int page(int entry) const { return hole(entry) ? 0 : entry; }
+  __device__ int slot(int t) const { return t & ((1 << lp) - 1); }
+};
 
-  f32x4 acc[kRowTiles][kOut] = {};
-  float m[kRowTiles], l[kRowTiles];  // m: the running maximum less kHeadroom
-#pragma unroll
-  for (int t = 0; t < kRowTiles; ++t) {
-    m[t] = kNoMax;
-    l[t] = 0.0f;
+// What a lane needs to know of its 16 tokens' scales.
+struct Scales {
+  float ks, vs;
+  bool hole;
+
+  __device__ void load(const Pages &p, int entry) {
+    hole = p.hole(entry);
+    const int64_t at = static_cast<int64_t>(p.page(entry)) * p.heads;
+    ks = p.k_scale[at];
+    vs = p.v_scale[at];
   }
+};
 
-  const int64_t page_bytes = static_cast<int64_t>(a.c.heads) * P * D;
-  const int8_t *kbase = a.c.k + static_cast<int64_t>(h) * P * D, *vbase = a.c.v + static_cast<int64_t>(h) * P * D;
-  const int step = kTeam ? 4 * kTile : kTile;
-  auto page_at = [&](int t) { return t < r.end ? page_of(a.s, b, t >> a.c.lp, a.c.pages) : -1; };
-  int t0 = r.begin + split * r.part * kTile + (kTeam ? wave * kTile : 0);
-  int kpage = -1, vpage = -1;
-  if (t0 < end) {
-    kpage = page_at(t0 + 16 * (n >> 2));
-    vpage = page_at(t0 + 16 * g);
-  }
-  for (; t0 < end; t0 += step) {
-    // Holes load page 0 in their place; their weights are zero.
-    const bool hole = vpage < 0;
-    const int64_t kp = kpage < 0 ? 0 : kpage, vp = hole ? 0 : vpage;
-    const float ks = hole ? 0.0f : a.c.k_scale[vp * a.c.heads + h];
-    const float vs = hole ? 1.0f : fmaxf(a.c.v_scale[vp * a.c.heads + h], kMinScale);
-    const int kslot = ((t0 + 16 * (n >> 2)) & (P - 1)) + (n & 3);
-    const int8_t *kptr = kbase + kp * page_bytes + kslot * D + 16 * g;
-    const int8_t *vptr = vbase + vp * page_bytes + n * P + ((t0 + 16 * g) & (P - 1));
-    i32x4 kc[4][kChunks], vc[kOut];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        kc[j][c] = i32x4{0, 0, 0, 0};
-        if (64 * c + 16 * g < D) kc[j][c] = *reinterpret_cast<const i32x4 *>(kptr + 4 * j * D + 64 * c);
-      }
-    }
-#pragma unroll
-    for (int d = 0; d < kOut; ++d) {
-      vc[d] = i32x4{0, 0, 0, 0};
-      if (16 * d < D) vc[d] = *reinterpret_cast<const i32x4 *>(vptr + 16 * d * P);
-    }
-    if (t0 + step < end) {
-      kpage = page_at(t0 + step + 16 * (n >> 2));
-      vpage = page_at(t0 + step + 16 * g);
-    }
-    const float lvs = hole ? -INFINITY : __log2f(vs), rvs = 1.0f / vs;
-    const bool edge = t0 < r.lo || t0 + kTile > r.hi;
-
-    union Weights {
-      f16x2 pair[8];
-      f16x8 half[2];
-    } w[kRowTiles][kParts];
-#pragma unroll
-    for (int t = 0; t < kRowTiles; ++t) {
-      float f[16];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        i32x4 dot[kDigits];
-#pragma unroll
-        for (int z = 0; z < kDigits; ++z) {
-          dot[z] = i32x4{0, 0, 0, 0};
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            dot[z] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kc[j][c], q[t][c][z], dot[z], 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (kDigits == 3) {
-            f[4 * j + i] = fmaf(static_cast<float>(dot[0][i]), 65536.0f, static_cast<float>(dot[1][i] * 256 + dot[2][i]));
-          } else {
-            f[4 * j + i] = static_cast<float>(dot[0][i] * 256 + dot[1][i]);
-          }
-        }
-      }
-      const float ck = qs[t] * ks;
-      float e[16];
-      auto exponents = [&](float base) {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) e[k] = fmaf(f[k], ck, base);
-        if (edge) {
-          const int under = lo[t] - (t0 + 16 * g), over = hi[t] - (t0 + 16 * g);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) e[k] = k >= under && k < over ? e[k] : -INFINITY;
-        }
-        float top = e[0];
-#pragma unroll
-        for (int k = 1; k < 16; ++k) top = fmaxf(top, e[k]);
-        return top;
-      };
-      float top = exponents(lvs - m[t]);
-      if (__any(top > kHeadroom)) {
-        top = over_lanes_max(exponents(lvs)) - kHeadroom;
-        const float now = fmaxf(m[t], top), shrink = __builtin_amdgcn_exp2f(m[t] - now);
-        m[t] = now;
-        l[t] *= shrink;
-#pragma unroll
-        for (int d = 0; d < kOut; ++d) acc[t][d] *= shrink;
-        exponents(lvs - now);
-      }
-      float sum = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 16; k += 2) {
-        const float p0 = __builtin_amdgcn_exp2f(e[k]), p1 = __builtin_amdgcn_exp2f(e[k + 1]);
-        sum += p0 + p1;
-        const f16x2 near = {static_cast<f16>(p0), static_cast<f16>(p1)};
-        w[t][0].pair[k / 2] = near;
-        if (kParts == 2)
-          w[t][kParts - 1].pair[k / 2] = f16x2{static_cast<f16>(p0 - static_cast<float>(near[0])),
-                                               static_cast<f16>(p1 - static_cast<float>(near[1]))};
-      }
-      l[t] = fmaf(sum, rvs, l[t]);
-    }
-#pragma unroll
-    for (int d = 0; d < kOut; ++d) {
-      if (16 * d >= D) continue;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        union {
-          f16x4 part[2];
-          f16x8 all;
-        } v;
-        v.part[0] = codes_to_f16(vc[d][2 * k]);
-        v.part[1] = codes_to_f16(vc[d][2 * k + 1]);
-#pragma unroll
-        for (int t = 0; t < kRowTiles; ++t) {
-#pragma unroll
-          for (int z = 0; z < kParts; ++z)
-            acc[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v.all, w[t][z].half[k], acc[t][d], 0, 0, 0);
-        }
-      }
-    }
-  }
-
-  // The lanes' sums, then (a team) the waves' results.
-#pragma unroll
-  for (int t = 0; t < kRowTiles; ++t) l[t] = over_lanes_sum(l[t]);
-  auto finish = [&](int t, int d, f32x4 o) {
-    if (at[t] < 0 || 16 * d >= D) return;
-    const int c = 16 * d + 4 * g;
-    if (r.used > 1) {
-      const int64_t row = static_cast<int64_t>(split) * a.s.rows * a.q_heads + at[t];
-      *reinterpret_cast<f32x4 *>(a.acc + row * D + c) = o;
-      if (d == 0 && g == 0) {
-        a.ml[2 * row] = m[t];
-        a.ml[2 * row + 1] = l[t];
-      }
-    } else {
-      const float inv = l[t] == 0.0f ? 0.0f : 1.0f / l[t];
-      const int64_t row = at[t] / a.q_heads, hq = at[t] - row * a.q_heads;
-      store4(static_cast<T *>(a.out) + row * a.out_stride + hq * D + c, o * inv);
-      if (d == 0 && g == 0 && a.lse) a.lse[at[t]] = l[t] == 0.0f ? -INFINITY : 0.69314718055994531f * (m[t] + log2f(l[t]));
-    }
+// A wave's rows: queries, running statistics, results.  Lane (n, g) holds row
+// n of each row tile; of a tile of tokens its logits are those of the 16
+// tokens 16 g .., of a result the components 16 d + 4 g ...
+template <typename T, int kChunks, bool kFull, int kRowTiles>
+struct Rows {
+  static constexpr int kDigits = std::is_same<T, bf16>::value ? 2 : 3;
+  static constexpr int kParts = kDigits - 1;             // f16 parts of a weight
+  static constexpr int kOut = 4 * kChunks;               // 16-component tiles
+  typedef typename Row<T>::Vec Vec;
+  static constexpr int kVecs = 16 / Row<T>::kValues;
+  union Weights {
+    f16x2 pair[8];
+    f16x8 half[2];
   };
-  if constexpr (kTeam) {
-    __shared__ f32x4 parts[4][kOut][64];
-    __shared__ float stats[4][16][2];
+
+  const Attend &a;
+  const int n, g, D;
+  f32x4 acc[kRowTiles][kOut];
+  i32x4 q[kRowTiles][kChunks][kDigits];
+  float qs[kRowTiles], m[kRowTiles], l[kRowTiles];  // m: the running maximum less kHeadroom
+  int lo[kRowTiles], hi[kRowTiles];
+  int row_of[kRowTiles], head_of[kRowTiles];        // row_of: -1 behind the last row
+  Vec qv[kRowTiles][kChunks][kVecs];
+
+  __device__ Rows(const Attend &args)
+      : a(args), n(threadIdx.x & 15), g((threadIdx.x & 63) >> 4), D(kFull ? 64 * kChunks : args.c.dim) {}
+
+  __device__ void place(const Place &w, int row0, int end) {
 #pragma unroll
     for (int t = 0; t < kRowTiles; ++t) {
-      if (t > 0) __syncthreads();
-      if (g == 0) {
-        stats[wave][n][0] = m[t];
-        stats[wave][n][1] = l[t];
-      }
-#pragma unroll
-      for (int d = 0; d < kOut; ++d) parts[wave][d][lane] = acc[t][d];
-      __syncthreads();
-      float wm[4], wl[4], now = kNoMax;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        wm[k] = stats[k][n][0];
-        wl[k] = stats[k][n][1];
-        now = fmaxf(now, wm[k]);
-      }
+      const int row = row0 + 16 * t + n;
+      const bool live = row < w.rows;
+      const int i = live ? row / a.group : 0;
+      const int64_t pos = static_cast<int64_t>(w.p.len) - w.p.n + i;
+      row_of[t] = live ? w.p.first + i : -1;
+      head_of[t] = w.h * a.group + (live ? row - i * a.group : 0);
+      hi[t] = !live ? 0 : a.causal ? clamp_int(pos + 1, end) : end;
+      lo[t] = a.window > 0 ? clamp_int(pos - a.window + 1, end) : 0;
+      qs[t] = 0.0f;
+      m[t] = kNoMax;
       l[t] = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        wm[k] = __builtin_amdgcn_exp2f(wm[k] - now);
-        l[t] = fmaf(wm[k], wl[k], l[t]);
-      }
-      m[t] = now;
+      for (int d = 0; d < kOut; ++d) acc[t][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int d = 0; d < kOut; ++d) {
-        if ((d & 3) != wave) continue;
-        f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int c = 0; c < kChunks; ++c) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o += wm[k] * parts[k][d][lane];
-        finish(t, d, o);
+        for (int z = 0; z < kDigits; ++z) q[t][c][z] = i32x4{0, 0, 0, 0};
       }
     }
-  } else {
+  }
+
+  __device__ void load_queries(const Place &w) {
 #pragma unroll
     for (int t = 0; t < kRowTiles; ++t) {
+      const T *src = static_cast<const T *>(a.q) + (row_of[t] < 0 ? w.p.first : row_of[t]) * a.q_stride +
+                     static_cast<int64_t>(head_of[t]) * D + 16 * g;
 #pragma unroll
-      for (int d = 0; d < kOut; ++d) finish(t, d, acc[t][d]);
+      for (int c = 0; c < kChunks; ++c) {
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+          qv[t][c][k] = Vec{};
+          if (kFull || 64 * c + 16 * g < D) qv[t][c][k] = reinterpret_cast<const Vec *>(src + 64 * c)[k];
+        }
+      }
     }
+  }
+
+  // The loaded queries as digits.
+  __device__ void set_queries() {
+#pragma unroll
+    for (int t = 0; t < kRowTiles; ++t) {
+      float v[kChunks][16];
+      float amax = 0.0f, nan = 0.0f;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          v[c][k] = static_cast<float>(qv[t][c][k / Row<T>::kValues][k % Row<T>::kValues]);
+          amax = fmaxf(amax, fabsf(v[c][k]));
+          nan = fmaf(v[c][k], 0.0f, nan);  // NaN once a component is a NaN or an infinity
+        }
+      }
+      if (nan != 0.0f) amax = INFINITY;
+      amax = over_lanes_max(amax);
+      constexpr float kTop = kDigits == 3 ? 127.0f * 65536.0f : 127.0f * 256.0f;
+      const float inv = amax > kMinScale && amax < INFINITY ? kTop / amax : 0.0f;
+      qs[t] = amax < INFINITY ? (amax > kMinScale ? amax / kTop * a.scale : 0.0f) : NAN;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          // With 128 added to every digit the digits are the sum's bytes.
+          uint32_t u[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            u[k] = static_cast<uint32_t>(static_cast<int>(rintf(v[c][4 * w + k] * inv)) + (kDigits == 3 ? 0x808080 : 0x8080));
+#pragma unroll
+          for (int z = 0; z < kDigits; ++z) {
+            const uint32_t byte = kDigits - 1 - z, pair = byte | (byte + 4) << 8 | 0x0c0c0000u;
+            const uint32_t low = __builtin_amdgcn_perm(u[1], u[0], pair), high = __builtin_amdgcn_perm(u[3], u[2], pair);
+            q[t][c][z][w] = static_cast<int>((low | high << 16) ^ 0x80808080u);
+          }
+        }
+      }
+    }
+  }
+
+  // Dots of row tile t with 16 tokens, K's operand given.
+  __device__ f32x4 dots(int t, const i32x4 (&k)[kChunks]) const {
+    i32x4 dot[kDigits];
+#pragma unroll
+    for (int z = 0; z < kDigits; ++z) {
+      dot[z] = i32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) dot[z] = __builtin_amdgcn_mfma_i32_16x16x64_i8(k[c], q[t][c][z], dot[z], 0, 0, 0);
+    }
+    f32x4 f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (kDigits == 3) {
+        f[i] = fmaf(static_cast<float>(dot[0][i]), 65536.0f, static_cast<float>(dot[1][i] * 256 + dot[kDigits - 1][i]));
+      } else {
+        f[i] = static_cast<float>(dot[0][i] * 256 + dot[1][i]);
+      }
+    }
+    return f;
+  }
+
+  // Weights of row tile t for the lane's tokens first .. first + 15, and the
+  // running statistics.  edge: some row of the wave does not see them all.
+  __device__ void weigh(int t, const f32x4 (&f)[4], const Scales &s, int first, bool edge, Weights (&w)[kParts]) {
+    const float vs = s.hole ? 1.0f : fmaxf(s.vs, kMinScale);
+    const float lvs = s.hole ? -INFINITY : __builtin_amdgcn_logf(vs), rvs = __builtin_amdgcn_rcpf(vs);
+    const float ck = qs[t] * (s.hole ? 0.0f : s.ks);
+    float e[16];
+    auto exponents = [&](float base) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) e[k] = fmaf(f[k / 4][k % 4], ck, base);
+      if (edge) {
+        const int under = lo[t] - first;
+        const unsigned width = hi[t] > lo[t] ? hi[t] - lo[t] : 0;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          e[k] = static_cast<unsigned>(k - under) < width ? e[k] : -INFINITY;
+          asm volatile("" : "+v"(e[k]));  // keeps this a branch: few tiles take it
+        }
+      }
+      float top = e[0];
+#pragma unroll
+      for (int k = 1; k < 16; ++k) top = fmaxf(top, e[k]);
+      return top;
+    };
+    float top = exponents(lvs - m[t]);
+    if (__any(top > kHeadroom)) {
+      top = over_lanes_max(exponents(lvs)) - kHeadroom;
+      const float now = fmaxf(m[t], top), shrink = __builtin_amdgcn_exp2f(m[t] - now);
+      m[t] = now;
+      l[t] *= shrink;
+#pragma unroll
+      for (int d = 0; d < kOut; ++d) acc[t][d] *= shrink;
+      exponents(lvs - now);
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {
+      const float p0 = __builtin_amdgcn_exp2f(e[k]), p1 = __builtin_amdgcn_exp2f(e[k + 1]);
+      sum += p0 + p1;
+      const f16x2 near = {static_cast<f16>(p0), static_cast<f16>(p1)};
+      w[0].pair[k / 2] = near;
+      if (kParts == 2) {
+        const f16x2 rest = {static_cast<f16>(less<0>(p0, near)), static_cast<f16>(less<1>(p1, near))};
+        w[kParts - 1].pair[k / 2] = rest;
+      }
+    }
+    l[t] = fmaf(sum, rvs, l[t]);
+  }
+
+  // acc += V^T P^T for 16 components and half of a tile's tokens.
+  __device__ void add(int t, int d, int half, f16x8 v, const Weights (&w)[kParts]) {
+#pragma unroll
+    for (int z = 0; z < kParts; ++z) acc[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, w[z].half[half], acc[t][d], 0, 0, 0);
+  }
+
+  // Results of row tile t to the output, or (several parts) to the workspace:
+  // value(i) gives the components of 16-component tile first + i * stride, for
+  // kCount of them.
+  template <int kCount, typename F>
+  __device__ void store(int t, int used, int split, int first, int stride, F value) const {
+    if (row_of[t] < 0) return;
+    const int64_t at = static_cast<int64_t>(row_of[t]) * a.q_heads + head_of[t];
+    const bool stats = first == 0 && g == 0;
+    if (used > 1) {
+      const int64_t row = static_cast<int64_t>(split) * a.s.rows * a.q_heads + at;
+      float *to = a.acc + row * D + 4 * g;
+#pragma unroll
+      for (int i = 0; i < kCount; ++i) {
+        const int d = first + i * stride;
+        if (kFull || 16 * d < D) *reinterpret_cast<f32x4 *>(to + 16 * d) = value(i);
+      }
+      if (stats) *reinterpret_cast<f32x2 *>(a.ml + 2 * row) = f32x2{m[t], l[t]};
+    } else {
+      const float inv = l[t] == 0.0f ? 0.0f : 1.0f / l[t];
+      T *to = static_cast<T *>(a.out) + row_of[t] * a.out_stride + static_cast<int64_t>(head_of[t]) * D + 4 * g;
+#pragma unroll
+      for (int i = 0; i < kCount; ++i) {
+        const int d = first + i * stride;
+        if (kFull || 16 * d < D) store4(to + 16 * d, value(i) * inv);
+      }
+      if (stats && a.lse) a.lse[at] = l[t] == 0.0f ? -INFINITY : kLn2 * (m[t] + log2f(l[t]));
+    }
+  }
+};
+
+__device__ inline f16x8 codes_to_f16(int low, int high) {
+  union {
+    f16x4 part[2];
+    f16x8 all;
+  } v;
+  v.part[0] = codes_to_f16(low);
+  v.part[1] = codes_to_f16(high);
+  return v.all;
+}
+
+// Few rows (a decode step): the workgroup's 4 waves share 16 rows, each takes
+// every fourth tile of tokens straight into registers, and their results are
+// joined through shared memory.  Bound by the cache's bytes: a tile's K is
+// loaded while the tile before it is weighted and multiplied by V, its V while
+// its own logits are formed, into the registers that the tile before has just
+// left; the pages are looked up one tile further ahead.
+// kChunks: 64-component chunks of a head, kFull: the head fills them.
+template <typename T, int kChunks, bool kFull>
+__global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_few_kernel(Attend a) {
+  typedef Rows<T, kChunks, kFull, 1> R;
+  constexpr int kOut = R::kOut, kWaves = kThreads / 64, kStep = kWaves * kTile;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  Place w;
+  if (!place_of(a, 16, w)) return;
+  const Range r = range_of(a, w.p, w.row0, (w.row0 + 16 < w.rows ? w.row0 + 16 : w.rows) - 1);
+  if (w.split >= (r.used > 1 ? r.used : 1)) return;
+  const Part part = part_of(r, w.split);
+  R rows(a);
+  rows.place(w, w.row0, r.end);
+  const int n = rows.n, g = rows.g, D = rows.D, kgroup = 16 * (n >> 2), P = 1 << a.c.lp;
+
+  int t0 = part.begin + wave * kTile;
+  if (t0 < part.end) {
+    const Pages pages(a, w.p.b, w.h, D, part.end);
+    i32x4 kc[4][kChunks], vc[kOut];
+    Scales next;
+    auto load_k = [&](int t, int entry) {
+      const int8_t *q = pages.k + pages.page(entry) * pages.bytes + (pages.slot(t + kgroup) + (n & 3)) * D + 16 * g;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          if (kFull || 64 * c + 16 * g < D) kc[j][c] = *reinterpret_cast<const i32x4 *>(q + 4 * j * D + 64 * c);
+        }
+      }
+    };
+    auto load_v = [&](int t, int entry) {
+      const int8_t *q = pages.v + pages.page(entry) * pages.bytes + n * P + pages.slot(t + 16 * g);
+#pragma unroll
+      for (int d = 0; d < kOut; ++d) {
+        if (kFull || 16 * d < D) vc[d] = *reinterpret_cast<const i32x4 *>(q + 16 * d * P);
+      }
+    };
+    if (!kFull) {
+#pragma unroll
+      for (int d = 0; d < kOut; ++d) vc[d] = kc[d & 3][d >> 2] = i32x4{0, 0, 0, 0};
+    }
+    rows.load_queries(w);
+    int kpage = pages.entry(t0 + kgroup), vpage = pages.entry(t0 + 16 * g);
+    const int kthen = pages.entry(t0 + kStep + kgroup), vthen = pages.entry(t0 + kStep + 16 * g);
+    load_k(t0, kpage);
+    next.load(pages, vpage);
+    load_v(t0, vpage);
+    kpage = kthen;
+    vpage = vthen;
+    __builtin_amdgcn_sched_barrier(0);
+    rows.set_queries();
+
+    for (; t0 < part.end; t0 += kStep) {
+      const Scales now = next;
+      f32x4 f[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = rows.dots(0, kc[j]);
+      // The order of loads is that of their uses: what waits for one waits for
+      // all before it.
+      load_k(t0 + kStep, kpage);
+      next.load(pages, vpage);
+      kpage = pages.entry(t0 + 2 * kStep + kgroup);
+      const int vthen = pages.entry(t0 + 2 * kStep + 16 * g);
+      typename R::Weights weights[R::kParts];
+      rows.weigh(0, f, now, t0 + 16 * g, t0 < r.lo || t0 + kTile > r.hi, weights);
+#pragma unroll
+      for (int d = 0; d < kOut; ++d) {
+        if (!kFull && 16 * d >= D) continue;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) rows.add(0, d, k, codes_to_f16(vc[d][2 * k], vc[d][2 * k + 1]), weights);
+      }
+      load_v(t0 + kStep, vpage);
+      vpage = vthen;
+    }
+  }
+
+  __shared__ f32x4 parts[kWaves][kOut][64];
+  __shared__ float stats[kWaves][16][2];
+  rows.l[0] = over_lanes_sum(rows.l[0]);
+  if (g == 0) {
+    stats[wave][n][0] = rows.m[0];
+    stats[wave][n][1] = rows.l[0];
+  }
+#pragma unroll
+  for (int d = 0; d < kOut; ++d) parts[wave][d][lane] = rows.acc[0][d];
+  __syncthreads();
+  float wm[kWaves], top = kNoMax;
+#pragma unroll
+  for (int k = 0; k < kWaves; ++k) {
+    wm[k] = stats[k][n][0];
+    top = fmaxf(top, wm[k]);
+  }
+  rows.l[0] = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kWaves; ++k) {
+    wm[k] = __builtin_amdgcn_exp2f(wm[k] - top);
+    rows.l[0] = fmaf(wm[k], stats[k][n][1], rows.l[0]);
+  }
+  rows.m[0] = top;
+  rows.template store<kOut / kWaves>(0, r.used, w.split, wave, kWaves, [&](int i) {
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) o += wm[k] * parts[k][wave + i * kWaves][lane];
+    return o;
+  });
+}
+
+// Many rows (prompts, drafted tokens): each of the workgroup's 4 waves has
+// kRowTiles x 16 rows of its own, and all walk the same tiles.  A wave loads a
+// quarter of the next tile's operands while the present one is worked on,
+// turns its part of V into f16 (once for the workgroup), and lays both down
+// in shared memory in the order in which lanes take them: 64 lanes x 16
+// bytes, free of bank conflicts.
+template <typename T, int kChunks, bool kFull, int kRowTiles>
+__global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_many_kernel(Attend a) {
+  typedef Rows<T, kChunks, kFull, kRowTiles> R;
+  constexpr int kOut = R::kOut, kRows = 16 * kRowTiles, kBlock = 4 * kRows;
+  __shared__ i32x4 lk[2][4][kChunks][64];
+  __shared__ f16x8 lv[2][kOut][2][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  Place w;
+  if (!place_of(a, kBlock, w)) return;
+  const int last = (w.row0 + kBlock < w.rows ? w.row0 + kBlock : w.rows) - 1;
+  const Range r = range_of(a, w.p, w.row0, last);
+  if (w.split >= (r.used > 1 ? r.used : 1)) return;
+  const Part part = part_of(r, w.split);
+  R rows(a);
+  const int row0 = w.row0 + wave * kRows;
+  rows.place(w, row0, r.end);
+  const int n = rows.n, g = rows.g, D = rows.D, kgroup = 16 * (n >> 2), P = 1 << a.c.lp;
+
+  if (part.begin < part.end) {
+    // Every row of this wave sees tokens own.lo .. own.hi - 1.
+    const Range own = range_of(a, w.p, row0 <= last ? row0 : last, row0 + kRows - 1 < last ? row0 + kRows - 1 : last);
+    const Pages pages(a, w.p.b, w.h, D, part.end);
+    i32x4 kc[kChunks], vc[kChunks];  // K's operand `wave`, V's components wave, wave + 4, ...
+    const bool whole = P >= kTile;  // a tile lies in one page
+    const int kplace = ((whole ? kgroup : 0) + (n & 3) + 4 * wave) * D + 16 * g, vplace = (n + 16 * wave) * P + (whole ? 16 * g : 0);
+    auto load = [&](int t, int kentry, int ventry) {
+      const int8_t *k, *v;
+      if (whole) {  // its address is the workgroup's
+        const int64_t at = pages.page(__builtin_amdgcn_readfirstlane(kentry)) * pages.bytes;
+        k = pages.k + at + pages.slot(t) * D + kplace;
+        v = pages.v + at + pages.slot(t) + vplace;
+      } else {
+        k = pages.k + pages.page(kentry) * pages.bytes + pages.slot(t + kgroup) * D + kplace;
+        v = pages.v + pages.page(ventry) * pages.bytes + pages.slot(t + 16 * g) + vplace;
+      }
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        if (kFull || 64 * c + 16 * g < D) kc[c] = *reinterpret_cast<const i32x4 *>(k + 64 * c);
+        if (kFull || 16 * (4 * c + wave) < D) vc[c] = *reinterpret_cast<const i32x4 *>(v + 64 * c * P);
+      }
+    };
+    auto lay_down = [&](int to) {
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        lk[to][wave][c][lane] = kc[c];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) lv[to][4 * c + wave][k][lane] = codes_to_f16(vc[c][2 * k], vc[c][2 * k + 1]);
+      }
+    };
+    if (!kFull) {
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) kc[c] = vc[c] = i32x4{0, 0, 0, 0};
+    }
+    rows.load_queries(w);
+    int t0 = part.begin;
+    Scales now, next;
+    int kpage = pages.entry(t0 + kgroup), vpage = pages.entry(t0 + 16 * g);
+    int vnext = pages.entry(t0 + kTile + 16 * g);
+    const int knext = pages.entry(t0 + kTile + kgroup);
+    load(t0, kpage, vpage);
+    now.load(pages, vpage);
+    __builtin_amdgcn_sched_barrier(0);
+    rows.set_queries();
+    lay_down(0);
+    load(t0 + kTile, knext, vnext);
+    kpage = pages.entry(t0 + 2 * kTile + kgroup);
+    vpage = pages.entry(t0 + 2 * kTile + 16 * g);
+    __syncthreads();
+
+    // What is carried on to the next round in other registers is loaded at a
+    // round's begin: the copies at its end then wait for nothing.
+    int kthen, vthen;
+    auto begin_round = [&]() {
+      next.load(pages, vnext);
+      kthen = pages.entry(t0 + 3 * kTile + kgroup);
+      vthen = pages.entry(t0 + 3 * kTile + 16 * g);
+    };
+    auto pass_on = [&](int to) {
+      lay_down(to);
+      load(t0 + 2 * kTile, kpage, vpage);
+    };
+    auto end_round = [&]() {
+      vnext = vpage;
+      kpage = kthen;
+      vpage = vthen;
+      now = next;
+      __syncthreads();
+    };
+    if (row0 > last) {  // no rows: this wave only fetches for the others
+      for (int from = 0; t0 < part.end; t0 += kTile, from ^= 1) {
+        begin_round();
+        pass_on(from ^ 1);
+        end_round();
+      }
+      return;
+    }
+    for (int from = 0; t0 < part.end; t0 += kTile, from ^= 1) {
+      begin_round();
+      typename R::Weights weights[kRowTiles][R::kParts];
+      const bool edge = t0 < own.lo || t0 + kTile > own.hi;
+      f32x4 f[kRowTiles][4];
+      i32x4 k[4][kChunks];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) k[j][c] = lk[from][j][c][lane];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int t = 0; t < kRowTiles; ++t) f[t][j] = rows.dots(t, k[j]);
+      }
+#pragma unroll
+      for (int t = 0; t < kRowTiles; ++t) rows.weigh(t, f[t], now, t0 + 16 * g, edge, weights[t]);
+      pass_on(from ^ 1);
+#pragma unroll
+      for (int d = 0; d < kOut; ++d) {
+        if (!kFull && 16 * d >= D) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const f16x8 v = lv[from][d][h][lane];
+#pragma unroll
+          for (int t = 0; t < kRowTiles; ++t) rows.add(t, d, h, v, weights[t]);
+        }
+      }
+      end_round();
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < kRowTiles; ++t) {
+    rows.l[t] = over_lanes_sum(rows.l[t]);
+    rows.template store<kOut>(t, r.used, w.split, 0, 1, [&](int d) { return rows.acc[t][d]; });
   }
 }
 
-// Joins the parts of rows that were split: one workgroup per row and head,
-// waves over parts, lanes over components.  unit: rows of the attention's tile.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) join_kernel(Attend a, int unit) {
-  __shared__ float sums[4][KV8_MAX_DIM], sl[4];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int row = blockIdx.x, hq = blockIdx.y, D = a.c.dim;
-  int b;
-  if (a.s.starts) {
-    b = last_at_most(a.s.seqs, row, [&](int i) { return start_of(a.s, i); });
-    if (b < 0) return;
-  } else {
-    b = row / a.s.per_seq;
+// Joins the parts of rows that were split.  A row and head is joined by
+// kTeams x 32 lanes, each four components of every kTeams-th part: 8 teams (a
+// workgroup) where there may be many parts, else one.
+// block_rows: rows of the attention's workgroups.
+template <typename T, int kTeams>
+__global__ void __launch_bounds__(kThreads) join_kernel(Attend a, int block_rows) {
+  constexpr int kItems = 8 / kTeams;  // rows and heads of a workgroup
+  __shared__ f32x4 sums[8][KV8_MAX_DIM / 4];
+  const int D = a.c.dim, lane = threadIdx.x & 31, team = kTeams > 1 ? threadIdx.x >> 5 : 0;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kItems + (kTeams > 1 ? 0 : threadIdx.x >> 5);
+  const int64_t each = static_cast<int64_t>(a.s.rows) * a.q_heads;
+  const int row = static_cast<int>((item < each ? item : each - 1) / a.q_heads), hq = static_cast<int>(item - static_cast<int64_t>(row) * a.q_heads);
+  // Rows of one workgroup may lie in two sequences: each wave looks for its
+  // first row's, then (rarely) on from there.
+  Span p = a.s.starts ? find(a.s, __builtin_amdgcn_readfirstlane(row), [](int, int start) { return start; })
+                      : span_of(a.s, row / a.s.per_seq);
+  if (a.s.starts && p.b >= 0) {
+    while (p.b + 1 < a.s.seqs && start_of(a.s, p.b + 1) <= row) p = span_of(a.s, p.b + 1);
   }
-  const Span p = span_of(a.s, b);
-  if (row >= p.first + p.n) return;
-  const int in_group = (row - p.first) * a.group + hq % a.group, row0 = in_group / unit * unit;
-  const int rows = p.n * a.group;
-  const Range r = range_of(a, p, row0, (row0 + unit < rows ? row0 + unit : rows) - 1);
-  if (r.used <= 1) return;
-  const int64_t each = static_cast<int64_t>(a.s.rows) * a.q_heads, at = static_cast<int64_t>(row) * a.q_heads + hq;
-  float now = kNoMax;
-  for (int k = lane; k < r.used; k += 64) now = fmaxf(now, a.ml[2 * (k * each + at)]);
-  now = wave_max(now);
-  float l = 0.0f, o[KV8_MAX_DIM / 64] = {};
-  for (int k = wave; k < r.used; k += 4) {
-    const int64_t from = k * each + at;
-    const float w = __builtin_amdgcn_exp2f(a.ml[2 * from] - now);
-    l = fmaf(w, a.ml[2 * from + 1], l);
+  bool live = item < each && p.b >= 0 && row >= p.first && row < p.first + p.n;
+  Range r = {};
+  if (live) {
+    const int in_group = (row - p.first) * a.group + hq % a.group, row0 = in_group / block_rows * block_rows;
+    const int rows = p.n * a.group;
+    r = range_of(a, p, row0, (row0 + block_rows < rows ? row0 + block_rows : rows) - 1);
+    live = r.used > 1;
+  }
+  if (kTeams > 1 && !live) return;  // the same for the whole workgroup
+  const int used = live ? r.used : 0;
+  const float *ml = a.ml + 2 * item, *acc = a.acc + item * D;
+  // The largest maximum and the denominator, by the team's lanes.
+  float now = kNoMax, l = 0.0f;
+  for (int k = lane; k < used; k += 32) now = fmaxf(now, ml[2 * k * each]);
 #pragma unroll
-    for (int i = 0; i < KV8_MAX_DIM / 64; ++i)
-      if (lane + 64 * i < D) o[i] = fmaf(w, a.acc[from * D + lane + 64 * i], o[i]);
+  for (int k = 1; k < 32; k *= 2) now = fmaxf(now, __shfl_xor(now, k));
+  for (int k = lane; k < used; k += 32) {
+    const f32x2 v = *reinterpret_cast<const f32x2 *>(ml + 2 * k * each);
+    l = fmaf(__builtin_amdgcn_exp2f(v[0] - now), v[1], l);
   }
 #pragma unroll
-  for (int i = 0; i < KV8_MAX_DIM / 64; ++i) sums[wave][lane + 64 * i] = o[i];
-  if (lane == 0) sl[wave] = l;
-  __syncthreads();
-  l = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+  for (int k = 1; k < 32; k *= 2) l += __shfl_xor(l, k);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  for (int d = threadIdx.x; d < D; d += kThreads)
-    static_cast<T *>(a.out)[row * a.out_stride + static_cast<int64_t>(hq) * D + d] =
-        static_cast<T>(((sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d])) * inv);
-  if (a.lse && threadIdx.x == 0) a.lse[at] = l == 0.0f ? -INFINITY : 0.69314718055994531f * (now + log2f(l));
+  T *out = static_cast<T *>(a.out) + row * a.out_stride + static_cast<int64_t>(hq) * D;
+  for (int c = lane; c < D / 4; c += 32) {
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int k = team; k < used; k += kTeams)
+      o += __builtin_amdgcn_exp2f(ml[2 * k * each] - now) * *reinterpret_cast<const f32x4 *>(acc + k * each * D + 4 * c);
+    if (kTeams > 1) {
+      sums[team][c] = o;
+    } else if (live) {
+      store4(out + 4 * c, o * inv);
+    }
+  }
+  if (kTeams > 1) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < D / 4; c += kThreads) {
+      f32x4 o = sums[0][c];
+#pragma unroll
+      for (int k = 1; k < kTeams; ++k) o += sums[k][c];
+      store4(out + 4 * c, o * inv);
+    }
+  }
+  if (a.lse && live && lane == 0 && team == 0) a.lse[item] = l == 0.0f ? -INFINITY : kLn2 * (now + log2f(l));
 }
 
 // ---------------------------------------------------------------------------
@@ -932,27 +1265,37 @@ inline int64_t slots(const Batch &s, int lp) {
   return static_cast<int64_t>(s.seqs) * (((s.per_seq + (INT64_C(1) << lp) - 2) >> lp) + 1);
 }
 
-// How an attention call is laid out: rows of a wave, whether a workgroup's
-// waves share them, and into how many parts the tokens are cut.
+// How an attention call is laid out: 16-row tiles of a wave (0: four waves
+// share one), rows of a workgroup, and into how many parts tokens are cut.
 struct Plan {
-  int row_tiles, splits;
-  bool team;
+  int row_tiles, block_rows, splits;
   int64_t blocks;  // workgroups along the rows
 };
 
 Plan plan_of(const Cache &c, const Batch &s, int64_t max_len, int64_t q_heads) {
   const int64_t group = q_heads / c.heads, rows = s.rows * group / s.seqs;  // of a sequence, on average
   Plan p;
-  p.team = rows <= 64;
-  p.row_tiles = rows <= 16 || c.dim > 128 ? 1 : 2;
-  const int64_t unit = 16 * p.row_tiles * (p.team ? 1 : 4);
-  p.blocks = s.starts ? s.rows * group / unit + s.seqs : (s.per_seq * group + unit - 1) / unit * s.seqs;
+  auto blocks_of = [&](int block_rows) {
+    return s.starts ? s.rows * group / block_rows + s.seqs : (s.per_seq * group + block_rows - 1) / block_rows * s.seqs;
+  };
+  p.row_tiles = 0;
+  if (rows > 16) {
+    // Two tiles of rows a wave read and turn V half as often, one leaves more
+    // workgroups to balance: 16 heads of width 64, prompts of 150 to 5000
+    // tokens, 172 against 185 us; 12 heads of width 128, one prompt of 4096
+    // tokens in F32 (386 workgroups of two tiles), 176 against 122 us.
+    p.row_tiles = c.dim <= 128 && rows > 64 && blocks_of(128) * c.heads >= 4 * kUnits ? 2 : 1;
+  }
+  p.block_rows = p.row_tiles ? 64 * p.row_tiles : 16;
+  p.blocks = blocks_of(p.block_rows);
   const int64_t held = static_cast<int64_t>(s.blocks) << c.lp;
   if (max_len <= 0 || max_len > held) max_len = held;
-  const int64_t most = (max_len + kTile * kMinPart - 1) / (kTile * kMinPart);
-  int64_t splits = 1024 / (p.blocks * c.heads);
+  // Up to two least parts are not worth a second launch (777 tokens: 11.0 us
+  // whole, 8.7 + 4.5 us in two parts).
+  const int64_t most = max_len <= 2 * kTile * kMinPart ? 1 : (max_len + kTile * kMinPart - 1) / (kTile * kMinPart);
+  int64_t splits = (p.row_tiles ? 5 : 8) * kUnits / (p.blocks * c.heads);
   if (splits > most) splits = most;
-  if (splits > 1024) splits = 1024;
+  if (splits > kMaxSplits) splits = kMaxSplits;
   p.splits = splits < 1 ? 1 : static_cast<int>(splits);
   return p;
 }
@@ -972,16 +1315,16 @@ inline size_t workspace_of(const Plan &p, const Cache &c, const Batch &s, int64_
   return p.splits > 1 ? static_cast<size_t>(p.splits) * s.rows * q_heads * (c.dim + 2) * sizeof(float) : 0;
 }
 
-template <typename T, int kChunks>
+template <typename T, int kChunks, bool kFull>
 int launch_attention(const Plan &p, const Attend &a, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(p.blocks), a.c.heads, p.splits);
+  const unsigned grid = static_cast<unsigned>(p.blocks * a.c.heads * p.splits);
   constexpr int kMost = kChunks > 2 ? 1 : 2;  // row tiles that fit the registers
-  if (p.team && p.row_tiles == 1) {
-    attention_kernel<T, kChunks, 1, true><<<grid, kThreads, 0, stream>>>(a);
-  } else if (p.team) {
-    attention_kernel<T, kChunks, kMost, true><<<grid, kThreads, 0, stream>>>(a);
+  if (p.row_tiles == 0) {
+    attention_few_kernel<T, kChunks, kFull><<<grid, kThreads, 0, stream>>>(a);
+  } else if (p.row_tiles == 1) {
+    attention_many_kernel<T, kChunks, kFull, 1><<<grid, kThreads, 0, stream>>>(a);
   } else {
-    attention_kernel<T, kChunks, kMost, false><<<grid, kThreads, 0, stream>>>(a);
+    attention_many_kernel<T, kChunks, kFull, kMost><<<grid, kThreads, 0, stream>>>(a);
   }
   return hip_status();
 }
@@ -1052,7 +1395,7 @@ extern "C" int kv8_attention(const kv8_cache *cache, const kv8_batch *batch, int
       !aligned(lse, 4))
     return I2S_EINVAL;
   const Plan p = plan_of(a.c, a.s, batch->max_len, q_heads);
-  if (p.blocks > 0x7fffffff) return I2S_ERANGE;
+  if (p.blocks * a.c.heads * p.splits > 0x7fffffff || rows * q_heads > 0x7fffffff) return I2S_ERANGE;
   const size_t need = workspace_of(p, a.c, a.s, q_heads);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return I2S_EWORKSPACE;
   a.q = q;
@@ -1068,14 +1411,23 @@ extern "C" int kv8_attention(const kv8_cache *cache, const kv8_batch *batch, int
   a.group = static_cast<int>(q_heads / a.c.heads);
   a.causal = causal != 0;
   a.splits = p.splits;
+  a.blocks = static_cast<int>(p.blocks);
+  a.round = kUnits / (a.c.heads * p.splits) > 1 ? kUnits / (a.c.heads * p.splits) : 1;
   const hipStream_t on = static_cast<hipStream_t>(stream);
   return by_type(type, [&](auto t) {
     typedef decltype(t) T;
-    const int st = a.c.dim <= 64    ? launch_attention<T, 1>(p, a, on)
-                   : a.c.dim <= 128 ? launch_attention<T, 2>(p, a, on)
-                                    : launch_attention<T, 4>(p, a, on);
+    const int st = a.c.dim == 128  ? launch_attention<T, 2, true>(p, a, on)
+                   : a.c.dim == 64 ? launch_attention<T, 1, true>(p, a, on)
+                   : a.c.dim < 64  ? launch_attention<T, 1, false>(p, a, on)
+                   : a.c.dim < 128 ? launch_attention<T, 2, false>(p, a, on)
+                                   : launch_attention<T, 4, false>(p, a, on);
     if (st || p.splits == 1) return st;
-    join_kernel<T><<<dim3(static_cast<unsigned>(rows), a.q_heads), kThreads, 0, on>>>(a, 16 * p.row_tiles);
+    const int64_t items = rows * q_heads;
+    if (p.splits > 8) {
+      join_kernel<T, 8><<<static_cast<unsigned>(items), kThreads, 0, on>>>(a, p.block_rows);
+    } else {
+      join_kernel<T, 1><<<static_cast<unsigned>((items + 7) / 8), kThreads, 0, on>>>(a, p.block_rows);
+    }
     return hip_status();
   });
 }
