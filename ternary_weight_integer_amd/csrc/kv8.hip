@@ -70,13 +70,6 @@ __device__ inline float wave_max(float v) {
                fmaxf(__int_as_float(__builtin_amdgcn_readlane(b, 32)), __int_as_float(__builtin_amdgcn_readlane(b, 48))));
 }
 
-__device__ inline float block_max(float v, float *red) {
-  v = wave_max(v);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-}
-
 // x rounded half away from zero, as a code.
 __device__ inline int code_of(float x) {
   return static_cast<int>(fminf(fmaxf(roundf(x), -127.0f), 127.0f));
@@ -185,47 +178,111 @@ struct Cache {
 };
 
 // ---------------------------------------------------------------------------
-// Append.  One workgroup per (page slot, head) and K or V: the maximum of the
-// page's new values, the page's scale, then the codes.
+// Append and read-back.
+//
+// One item is a page slot, a head, and K or V.  A lane works on units of
+// kTokens (8 or 16) tokens x 4 components: 32 neighbouring lanes cover a row of 128 components,
+// so rows are read and written in whole lines, and V's turning (tokens
+// innermost in the page) is 4 x 4 byte transposes within the lane.  A wave has
+// 64 units at a time; an item has as many waves as its units fill, up to the
+// workgroup's 4.
+
+constexpr int kUnitDims = 4, kFewTokens = 4;
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) append_kernel(Cache c, Batch s, const T *__restrict__ kx, int64_t k_stride,
-                                                          const T *__restrict__ vx, int64_t v_stride) {
-  extern __shared__ int8_t tile[];  // V: [new tokens][dim] codes
-  __shared__ float red[4];
+struct Four {
+  typedef T Vec __attribute__((ext_vector_type(4)));
+};
+
+// Transposes 4 x 4 bytes: byte j of row i becomes byte i of row j.
+__device__ inline void transpose4(uint32_t (&r)[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(r[1], r[0], 0x05010400u), b = __builtin_amdgcn_perm(r[1], r[0], 0x07030602u);
+  const uint32_t c = __builtin_amdgcn_perm(r[3], r[2], 0x05010400u), d = __builtin_amdgcn_perm(r[3], r[2], 0x07030602u);
+  r[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
+  r[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
+  r[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
+  r[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
+}
+
+__device__ inline uint32_t pack_bytes(uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3) {
+  const uint32_t lo = __builtin_amdgcn_perm(b1, b0, 0x0c0c0400u), hi = __builtin_amdgcn_perm(b3, b2, 0x0c0c0400u);
+  return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+}
+
+// Four codes round_half_away(x / s), |x| <= 127 s.  The division is replaced by
+// a product with inv = 1 / s wherever that gives the same code: x * inv and
+// x / s, each rounded, lie within 2^-18 + 1.6e-5 of the quotient, so where the
+// product's fraction is more than 2^-14 from 1/2 both round to its nearest
+// integer.  Adding 1.5 * 2^23 rounds to that integer and leaves its byte lowest.
+__device__ inline uint32_t codes_of(const float (&x)[4], float s, float inv) {
+  float r[4];
+  bool near = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    r[j] = x[j] * inv;
+    near |= fabsf(__builtin_amdgcn_fractf(fabsf(r[j])) - 0.5f) <= 0x1p-14f;
+  }
+  if (near) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = static_cast<float>(code_of(x[j] / s));
+  }
+  uint32_t b[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(r[j] + 0x1.8p23f);
+  return pack_bytes(b[0], b[1], b[2], b[3]);
+}
+
+// Four codes round_half_away(q * ratio) of codes q.
+__device__ inline uint32_t rescaled(uint32_t q, float ratio) {
+  uint32_t b[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    b[j] = static_cast<uint32_t>(static_cast<int>(roundf(static_cast<float>(static_cast<int8_t>(q >> (8 * j))) * ratio)));
+  return pack_bytes(b[0], b[1], b[2], b[3]);
+}
+
+// An item: the tokens [t0, t1) that it holds of the call's rows, in slots
+// lo .. lo + n - 1 of its page.
+struct Item {
+  int b, h, lo, n;
+  bool value;
+  int page;     // -1: a hole
+  int64_t row;  // of token t0
+  int ahead, first;  // rows in front of position 0 (at the sequence's first slot), and the first of them
+};
+
+__device__ inline bool item_of(const Cache &c, const Batch &s, int64_t index, Item &it) {
+  it.n = it.ahead = 0;
+  it.page = -1;
+  it.value = index & 1;
+  const int slot = static_cast<int>((index >> 1) / c.heads);
+  it.h = static_cast<int>((index >> 1) - static_cast<int64_t>(slot) * c.heads);
   Span p;
   int64_t j;
-  if (!slot_of(s, c.lp, blockIdx.x, p, j)) return;
-  const int P = 1 << c.lp, D = c.dim, h = blockIdx.y;
+  if (!slot_of(s, c.lp, slot, p, j)) return false;
   const int64_t done = static_cast<int64_t>(p.len) - p.n, begin = j << c.lp;
-  int64_t t0 = done > begin ? done : begin, t1 = begin + P;
+  it.b = p.b;
+  it.first = p.first;
+  if (done < 0 && begin == 0) it.ahead = static_cast<int>(-done < p.n ? -done : p.n);
+  int64_t t0 = done > begin ? done : begin, t1 = begin + (1 << c.lp);
   if (t0 < 0) t0 = 0;
   if (t1 > p.len) t1 = p.len;
-  if (t0 >= t1) return;
-  const int page = page_of(s, p.b, j, c.pages);
-  if (page < 0) return;
-  const bool value = blockIdx.z != 0;
-  const int64_t stride = value ? v_stride : k_stride;
-  const T *src = (value ? vx : kx) + (p.first + (t0 - done)) * stride + static_cast<int64_t>(h) * D;
-  const int64_t at = static_cast<int64_t>(page) * c.heads + h;
-  float *scale = (value ? c.v_scale : c.k_scale) + at;
-  int8_t *codes = (value ? c.v : c.k) + at * P * D;
-  const int n = static_cast<int>(t1 - t0), lo = static_cast<int>(t0 - begin), per = D / 16, units = n * per;
-
-  float amax = 0.0f;
-  for (int u = threadIdx.x; u < units; u += kThreads) {
-    const T *q = src + (u / per) * stride + (u % per) * 16;
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 16; i += Row<T>::kValues) load16(q + i, x + i);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+  if (t0 < t1) {
+    it.n = static_cast<int>(t1 - t0);
+    it.lo = static_cast<int>(t0 - begin);
+    it.row = p.first + (t0 - done);
+    it.page = page_of(s, p.b, j, c.pages);
   }
-  amax = block_max(amax, red);
-  float now = fmaxf(amax, kAmaxFloor) / 127.0f, ratio = 1.0f;
-  bool grown = false;
-  if (lo > 0) {
-    const float before = *scale;
+  return true;
+}
+
+// A page's scale after new values of maximum amax; ratio: of its earlier codes.
+struct Scaling {
+  float now, ratio;
+  bool grown;
+
+  __device__ Scaling(float amax, float before, bool begun) : now(fmaxf(amax, kAmaxFloor) / 127.0f), ratio(1.0f), grown(false) {
+    if (!begun) return;
     if (now > before) {
       grown = true;
       ratio = before / now;
@@ -233,135 +290,234 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Cache c, Batch s, cons
       now = before;
     }
   }
-  __syncthreads();  // the old scale is read before it is written
-  if (threadIdx.x == 0) *scale = now;
+};
 
-  for (int u = threadIdx.x; u < units; u += kThreads) {
-    const int t = u / per, d = (u % per) * 16;
-    float x[16];
+// Few new tokens (a decode step): one wave, a lane four components of each
+// token.  Nothing is read back unless the scale grew, V's new codes are single
+// bytes: for 48 sequences of one token 8 heads took 17.6 us by whole units.
+template <typename T>
+__device__ inline void append_few(const T *src, int64_t stride, int8_t *codes, float *scale, int P, int D, int lo, int n, bool value) {
+  typedef typename Four<T>::Vec Vec;
+  const int lane = threadIdx.x & 63, d = kUnitDims * lane;
+  Vec x[kFewTokens];
+  float before = 0.0f, amax = 0.0f;
+  if (lo > 0) before = *scale;
 #pragma unroll
-    for (int i = 0; i < 16; i += Row<T>::kValues) load16(src + t * stride + d + i, x + i);
-    union {
-      int8_t b[16];
-      i32x4 v;
-    } q;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) q.b[i] = static_cast<int8_t>(code_of(x[i] / now));
-    int8_t *to = value ? tile + t * D + d : codes + (lo + t) * D + d;
-    *reinterpret_cast<i32x4 *>(to) = q.v;
+  for (int i = 0; i < kFewTokens; ++i) {
+    x[i] = Vec{};
+    if (i < n && d < D) x[i] = *reinterpret_cast<const Vec *>(src + i * stride + d);
   }
-  if (!value) {
-    if (grown) {
-      for (int u = threadIdx.x; u < lo * per; u += kThreads) {
-        union {
-          int8_t b[16];
-          i32x4 v;
-        } q;
-        q.v = reinterpret_cast<i32x4 *>(codes)[u];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) q.b[i] = static_cast<int8_t>(roundf(static_cast<float>(q.b[i]) * ratio));
-        reinterpret_cast<i32x4 *>(codes)[u] = q.v;
-      }
-    }
-    return;
+  for (int i = 0; i < kFewTokens; ++i) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fabsf(static_cast<float>(x[i][k])));
   }
-  __syncthreads();
-  const int chunks = P / 16;  // of a component's row, 16 tokens each
-  for (int u = threadIdx.x; u < D * chunks; u += kThreads) {
-    const int d = u / chunks, s0 = (u % chunks) * 16;
-    const bool has_new = s0 < lo + n && s0 + 16 > lo, has_old = s0 < lo;
-    if (!has_new && !(grown && has_old)) continue;
-    union {
-      int8_t b[16];
-      i32x4 v;
-    } q;
-    i32x4 *to = reinterpret_cast<i32x4 *>(codes + d * P + s0);
-    q.v = *to;
+  const Scaling s(wave_max(amax), before, lo > 0);
+  if (lane == 0 && s.now != before) *scale = s.now;
+  if (s.grown) {
+    const int row = value ? P : D, count = value ? D * P / 16 : lo * D / 16;
+    for (int u = lane; u < count; u += 64) {
+      const int slot = value ? 16 * u % row : 0;
+      if (slot >= lo && value) continue;
+      i32x4 *at = reinterpret_cast<i32x4 *>(codes) + u;
+      i32x4 q = *at;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int slot = s0 + i;
-      if (slot < lo) {
-        if (grown) q.b[i] = static_cast<int8_t>(roundf(static_cast<float>(q.b[i]) * ratio));
-      } else if (slot < lo + n) {
-        q.b[i] = tile[(slot - lo) * D + d];
+      for (int w = 0; w < 4; ++w) {
+        // Codes behind the earlier tokens keep their bytes.
+        const int left = value ? lo - slot - 4 * w : 4;
+        const uint32_t mask = left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1;
+        const uint32_t old = static_cast<uint32_t>(q[w]);
+        q[w] = static_cast<int>((old & ~mask) | (rescaled(old, s.ratio) & mask));
       }
+      *at = q;
     }
-    *to = q.v;
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
+    __builtin_amdgcn_s_waitcnt(0);  // before single bytes of the same 16 are written
+  }
+  if (d >= D) return;
+  const float inv = 1.0f / s.now;
+#pragma unroll
+  for (int i = 0; i < kFewTokens; ++i) {
+    if (i >= n) continue;
+    const float v[4] = {static_cast<float>(x[i][0]), static_cast<float>(x[i][1]), static_cast<float>(x[i][2]),
+                        static_cast<float>(x[i][3])};
+    const uint32_t code = codes_of(v, s.now, inv);
+    if (!value) {
+      *reinterpret_cast<uint32_t *>(codes + (lo + i) * D + d) = code;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) codes[(d + k) * P + lo + i] = static_cast<int8_t>(code >> (8 * k));
+    }
   }
 }
 
-// ---------------------------------------------------------------------------
-// Read back.  One workgroup per (page slot, head); V's codes are turned
-// through shared memory.
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) read_kernel(Cache c, Batch s, T *__restrict__ ko, int64_t k_stride,
-                                                        T *__restrict__ vo, int64_t v_stride) {
-  extern __shared__ int8_t tile[];  // [P][dim]
-  Span p;
-  int64_t j;
-  if (!slot_of(s, c.lp, blockIdx.x, p, j)) return;
-  const int P = 1 << c.lp, D = c.dim, h = blockIdx.y, per = D / 16;
-  const int64_t done = static_cast<int64_t>(p.len) - p.n, begin = j << c.lp;
-  ko += static_cast<int64_t>(h) * D;
-  vo += static_cast<int64_t>(h) * D;
-  float zero[16] = {};
-  if (done < 0 && begin == 0) {  // rows in front of position 0
-    const int64_t ahead = -done < p.n ? -done : p.n;
-    for (int64_t u = threadIdx.x; u < ahead * per; u += kThreads) {
-      const int64_t row = p.first + u / per, d = (u % per) * 16;
+// Append: the maximum of the item's new values, the page's scale, then the
+// codes.  kOnce: the item's units fill its waves once, and the values stay in
+// registers between the two; else they are read again (from the cache).
+template <typename T, int kTokens, bool kOnce>
+__global__ void __launch_bounds__(kThreads) append_kernel(Cache c, Batch s, const T *__restrict__ kx, int64_t k_stride,
+                                                          const T *__restrict__ vx, int64_t v_stride, int waves,
+                                                          int64_t items) {
+  __shared__ float red[kThreads / 64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int64_t index = static_cast<int64_t>(blockIdx.x) * (4 / waves) + wave / waves;
+  Item it;
+  const bool live = index < items && item_of(c, s, index, it) && it.n > 0 && it.page >= 0;
+  const bool few = live && it.n <= kFewTokens;
+  const int P = 1 << c.lp, D = c.dim, per = D / kUnitDims, units = live && !few ? P / kTokens * per : 0;
+  const int64_t stride = live && it.value ? v_stride : k_stride;
+  const T *src = (live && it.value ? vx : kx) + (live ? it.row * stride + static_cast<int64_t>(it.h) * D : 0);
+  const int64_t at = live ? static_cast<int64_t>(it.page) * c.heads + it.h : 0;
+  float *scale = (live && it.value ? c.v_scale : c.k_scale) + at;
+  int8_t *codes = (live && it.value ? c.v : c.k) + at * P * D;
+  const int lo = live ? it.lo : 0, end = live ? it.lo + it.n : 0;
+  const int first = (wave % waves) * 64 + lane, step = waves * 64;
+  if (few && wave % waves == 0) append_few(src, stride, codes, scale, P, D, lo, it.n, it.value);
+  typedef typename Four<T>::Vec Vec;
+  typedef int Tokens __attribute__((ext_vector_type(kTokens / 4)));  // a component's codes in a unit
+  Vec x[kTokens];
+  auto load = [&](int u) {
+    const int d = u % per * kUnitDims, s0 = u / per * kTokens;
 #pragma unroll
-      for (int i = 0; i < 16; i += Row<T>::kValues) {
-        store16(ko + row * k_stride + d + i, zero);
-        store16(vo + row * v_stride + d + i, zero);
+    for (int i = 0; i < kTokens; ++i) {
+      x[i] = Vec{};
+      if (s0 + i >= lo && s0 + i < end) x[i] = *reinterpret_cast<const Vec *>(src + (s0 + i - lo) * stride + d);
+    }
+  };
+  const float before = units > 0 && lo > 0 ? *scale : 0.0f;
+  float amax = 0.0f;
+  for (int u = first; u < units; u += step) {
+    load(u);
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fabsf(static_cast<float>(x[i][k])));
+    }
+  }
+  amax = wave_max(amax);
+  if (lane == 0) red[wave] = amax;
+  __syncthreads();  // the old scale has been read, too
+  if (units == 0) return;
+  for (int k = 0; k < waves; ++k) amax = fmaxf(amax, red[wave / waves * waves + k]);
+  const Scaling scaling(amax, before, lo > 0);
+  const float now = scaling.now, ratio = scaling.ratio, inv = 1.0f / now;
+  const bool grown = scaling.grown;
+  if (first == 0) *scale = now;
+  for (int u = first; u < units; u += step) {
+    const int d = u % per * kUnitDims, s0 = u / per * kTokens;
+    const bool has_new = s0 < end && s0 + kTokens > lo, has_old = grown && s0 < lo;
+    if (!has_new && !has_old) continue;
+    if (!kOnce) load(u);
+    uint32_t code[kTokens];  // a token's four components
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = static_cast<float>(x[i][k]);
+      code[i] = codes_of(v, now, inv);  // 0 outside the new tokens
+    }
+    if (!it.value) {
+      uint32_t *to = reinterpret_cast<uint32_t *>(codes + s0 * D + d);
+#pragma unroll
+      for (int i = 0; i < kTokens; ++i) {
+        if (s0 + i >= lo && s0 + i < end) {
+          to[i * per] = code[i];
+        } else if (grown && s0 + i < lo) {
+          to[i * per] = rescaled(to[i * per], ratio);
+        }
+      }
+    } else {
+      const bool whole = s0 >= lo && s0 + kTokens <= end;
+      Tokens row[4];  // of a component
+#pragma unroll
+      for (int i = 0; i < kTokens / 4; ++i) {
+        uint32_t r[4] = {code[4 * i], code[4 * i + 1], code[4 * i + 2], code[4 * i + 3]};
+        transpose4(r);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) row[k][i] = static_cast<int>(r[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        Tokens *to = reinterpret_cast<Tokens *>(codes + (d + k) * P + s0);
+        if (!whole) {
+          const Tokens old = *to;
+#pragma unroll
+          for (int i = 0; i < kTokens / 4; ++i) {
+            uint32_t kept = static_cast<uint32_t>(old[i]), mask = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int slot = s0 + 4 * i + j;
+              if (slot >= lo && slot < end) mask |= 0xffu << (8 * j);
+            }
+            if (grown && s0 + 4 * i < lo) {
+              const uint32_t moved = rescaled(kept, ratio);
+              uint32_t gone = 0;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (s0 + 4 * i + j < lo) gone |= 0xffu << (8 * j);
+              kept = (kept & ~gone) | (moved & gone);
+            }
+            row[k][i] = static_cast<int>((kept & ~mask) | (static_cast<uint32_t>(row[k][i]) & mask));
+          }
+        }
+        *to = row[k];
       }
     }
   }
-  int64_t t0 = done > begin ? done : begin, t1 = begin + P;
-  if (t0 < 0) t0 = 0;
-  if (t1 > p.len) t1 = p.len;
-  if (t0 >= t1) return;
-  const int page = page_of(s, p.b, j, c.pages);
-  const int n = static_cast<int>(t1 - t0), lo = static_cast<int>(t0 - begin);
-  const int64_t row0 = p.first + (t0 - done), at = static_cast<int64_t>(page) * c.heads + h;
-  float ks = 0.0f, vs = 0.0f;
-  if (page >= 0) {
-    ks = c.k_scale[at];
-    vs = c.v_scale[at];
-    const int chunks = P / 16;
-    for (int u = threadIdx.x; u < D * chunks; u += kThreads) {
-      const int d = u / chunks, s0 = (u % chunks) * 16;
-      union {
-        int8_t b[16];
-        i32x4 v;
-      } q;
-      q.v = *reinterpret_cast<const i32x4 *>(c.v + at * P * D + d * P + s0);
+}
+
+// Read-back, the inverse.
+template <typename T, int kTokens>
+__global__ void __launch_bounds__(kThreads) read_kernel(Cache c, Batch s, T *__restrict__ ko, int64_t k_stride,
+                                                        T *__restrict__ vo, int64_t v_stride, int waves, int64_t items) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int64_t index = static_cast<int64_t>(blockIdx.x) * (4 / waves) + wave / waves;
+  Item it;
+  if (index >= items || !item_of(c, s, index, it)) return;
+  const int P = 1 << c.lp, D = c.dim, per = D / kUnitDims, first = (wave % waves) * 64 + lane, step = waves * 64;
+  const int64_t stride = it.value ? v_stride : k_stride;
+  T *out = (it.value ? vo : ko) + static_cast<int64_t>(it.h) * D;
+  typedef typename Four<T>::Vec Vec;
+  typedef int Tokens __attribute__((ext_vector_type(kTokens / 4)));  // a component's codes in a unit
+  for (int64_t u = first; u < static_cast<int64_t>(it.ahead) * per; u += step)
+    *reinterpret_cast<Vec *>(out + (it.first + u / per) * stride + u % per * kUnitDims) = Vec{};
+  if (it.n == 0) return;
+  const int units = P / kTokens * per, end = it.lo + it.n;
+  const int64_t at = static_cast<int64_t>(it.page < 0 ? 0 : it.page) * c.heads + it.h;
+  const float scale = it.page < 0 ? 0.0f : (it.value ? c.v_scale : c.k_scale)[at];
+  const int8_t *codes = (it.value ? c.v : c.k) + at * P * D;
+  out += it.row * stride;
+  for (int u = first; u < units; u += step) {
+    const int d = u % per * kUnitDims, s0 = u / per * kTokens;
+    if (s0 >= end || s0 + kTokens <= it.lo) continue;
+    uint32_t code[kTokens];
+    if (!it.value) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) tile[(s0 + i) * D + d] = q.b[i];
-    }
-    __syncthreads();
-  }
-  for (int u = threadIdx.x; u < n * per; u += kThreads) {
-    const int t = u / per, d = (u % per) * 16;
-    union {
-      int8_t b[16];
-      i32x4 v;
-    } qk, qv;
-    qk.v = qv.v = i32x4{0, 0, 0, 0};
-    if (page >= 0) {
-      qk.v = *reinterpret_cast<const i32x4 *>(c.k + at * P * D + (lo + t) * D + d);
-      qv.v = *reinterpret_cast<const i32x4 *>(tile + (lo + t) * D + d);
-    }
-    float xk[16], xv[16];
+      for (int i = 0; i < kTokens; ++i) code[i] = *reinterpret_cast<const uint32_t *>(codes + (s0 + i) * D + d);
+    } else {
+      Tokens row[4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      xk[i] = static_cast<float>(qk.b[i]) * ks;
-      xv[i] = static_cast<float>(qv.b[i]) * vs;
+      for (int k = 0; k < 4; ++k) row[k] = *reinterpret_cast<const Tokens *>(codes + (d + k) * P + s0);
+#pragma unroll
+      for (int i = 0; i < kTokens / 4; ++i) {
+        uint32_t r[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r[k] = static_cast<uint32_t>(row[k][i]);
+        transpose4(r);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) code[4 * i + k] = r[k];
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 16; i += Row<T>::kValues) {
-      store16(ko + (row0 + t) * k_stride + d + i, xk + i);
-      store16(vo + (row0 + t) * v_stride + d + i, xv + i);
+    for (int i = 0; i < kTokens; ++i) {
+      if (s0 + i < it.lo || s0 + i >= end) continue;
+      Vec v;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float q = static_cast<float>(static_cast<int8_t>(code[i] >> (8 * k)));
+        v[k] = static_cast<T>(it.page < 0 ? 0.0f : q * scale);
+      }
+      *reinterpret_cast<Vec *>(out + (s0 + i - it.lo) * stride + d) = v;
     }
   }
 }
@@ -1265,6 +1421,27 @@ inline int64_t slots(const Batch &s, int lp) {
   return static_cast<int64_t>(s.seqs) * (((s.per_seq + (INT64_C(1) << lp) - 2) >> lp) + 1);
 }
 
+// How an append or a read-back is laid out: tokens of a unit, units and waves
+// of an item, all items and the workgroups that hold them.
+struct Items {
+  int tokens, units, waves;
+  int64_t items, blocks;
+
+  Items(const Cache &c, const Batch &s, bool append) {
+    items = slots(s, c.lp) * c.heads * 2;
+    // Reading back, units of 16 tokens move whole 16-byte pieces of V's rows
+    // (84 against 91 us for 65536 x 8 x 128 values, BF16), units of 8 make more
+    // waves where there are few (5.6 against 6.5 us for 1100 x 2 x 128, F32).
+    // Appending holds a unit's values in registers: 8.
+    tokens = append || items << c.lp < (INT64_C(1) << 19) ? 8 : 16;
+    units = (1 << c.lp) / tokens * (c.dim / kUnitDims);
+    waves = units <= 64 ? 1 : units <= 128 ? 2 : 4;
+    // A decode step's items are one wave's work.
+    if (append && s.rows <= kFewTokens * s.seqs) waves = 1;
+    blocks = (items * waves + 3) / 4;
+  }
+};
+
 // How an attention call is laid out: 16-row tiles of a wave (0: four waves
 // share one), rows of a workgroup, and into how many parts tokens are cut.
 struct Plan {
@@ -1346,13 +1523,19 @@ extern "C" int kv8_append(const kv8_cache *cache, const kv8_batch *batch, int ty
   if (rows == 0 || s.seqs == 0) return I2S_OK;
   const int64_t width = static_cast<int64_t>(c.heads) * c.dim;
   if (bad_rows(k, k_stride, width, value_bytes(type)) || bad_rows(v, v_stride, width, value_bytes(type))) return I2S_EINVAL;
-  const int64_t n = slots(s, c.lp);
-  if (n > 0x7fffffff) return I2S_ERANGE;
+  const Items n(c, s, true);
+  if (n.blocks > 0x7fffffff) return I2S_ERANGE;
   return by_type(type, [&](auto t) {
     typedef decltype(t) T;
-    append_kernel<T><<<dim3(static_cast<unsigned>(n), c.heads, 2), kThreads, static_cast<size_t>(c.dim) << c.lp,
-                       static_cast<hipStream_t>(stream)>>>(c, s, static_cast<const T *>(k), k_stride,
-                                                           static_cast<const T *>(v), v_stride);
+    auto launch = [&](auto kernel) {
+      kernel<<<static_cast<unsigned>(n.blocks), kThreads, 0, static_cast<hipStream_t>(stream)>>>(
+          c, s, static_cast<const T *>(k), k_stride, static_cast<const T *>(v), v_stride, n.waves, n.items);
+    };
+    if (n.units <= 64 * n.waves) {
+      launch(append_kernel<T, 8, true>);
+    } else {
+      launch(append_kernel<T, 8, false>);
+    }
     return hip_status();
   });
 }
@@ -1365,12 +1548,19 @@ extern "C" int kv8_read(const kv8_cache *cache, const kv8_batch *batch, int type
   if (rows == 0 || s.seqs == 0) return I2S_OK;
   const int64_t width = static_cast<int64_t>(c.heads) * c.dim;
   if (bad_rows(k, k_stride, width, value_bytes(type)) || bad_rows(v, v_stride, width, value_bytes(type))) return I2S_EINVAL;
-  const int64_t n = slots(s, c.lp);
-  if (n > 0x7fffffff) return I2S_ERANGE;
+  const Items n(c, s, false);
+  if (n.blocks > 0x7fffffff) return I2S_ERANGE;
   return by_type(type, [&](auto t) {
     typedef decltype(t) T;
-    read_kernel<T><<<dim3(static_cast<unsigned>(n), c.heads), kThreads, static_cast<size_t>(c.dim) << c.lp,
-                     static_cast<hipStream_t>(stream)>>>(c, s, static_cast<T *>(k), k_stride, static_cast<T *>(v), v_stride);
+    auto launch = [&](auto kernel) {
+      kernel<<<static_cast<unsigned>(n.blocks), kThreads, 0, static_cast<hipStream_t>(stream)>>>(
+          c, s, static_cast<T *>(k), k_stride, static_cast<T *>(v), v_stride, n.waves, n.items);
+    };
+    if (n.tokens == 16) {
+      launch(read_kernel<T, 16>);
+    } else {
+      launch(read_kernel<T, 8>);
+    }
     return hip_status();
   });
 }

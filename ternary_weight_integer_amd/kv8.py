@@ -87,7 +87,8 @@ class KV8Cache:
     """A cache's tensors: k int8 [pages][heads][P][dim], v int8
     [pages][heads][dim][P], k_scale and v_scale F32 [pages][heads]."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "heads", "dim", "page_tokens", "device", "_c", "_ref")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "heads", "dim", "page_tokens", "device", "index", "scale",
+                 "_c", "_ref")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
         _need(k, torch.int8, 4, "k")
@@ -105,7 +106,7 @@ class KV8Cache:
                 raise ValueError(f"{name} is on another device than k")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.heads, self.dim, self.page_tokens = pages, heads, dim, page_tokens
-        self.device = k.device
+        self.device, self.index, self.scale = k.device, k.get_device(), dim ** -0.5
         self._c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, heads, dim, page_tokens)
         self._ref = ctypes.addressof(self._c)
 
@@ -123,7 +124,7 @@ class KV8Batch:
     starts None (every sequence has as many rows) or int32 [seqs + 1].
     max_len: 0, or a bound of the lengths; it steers the attention's split."""
 
-    __slots__ = ("table", "lens", "starts", "max_len", "seqs", "device", "_c", "_ref")
+    __slots__ = ("table", "lens", "starts", "max_len", "seqs", "index", "_c", "_ref")
 
     def __init__(self, table: torch.Tensor, lens: torch.Tensor, starts: torch.Tensor | None = None, max_len: int = 0):
         _need(table, torch.int32, 2, "table")
@@ -140,120 +141,130 @@ class KV8Batch:
         if lens.device != table.device or (starts is not None and starts.device != table.device):
             raise ValueError("table, lens and starts are on different devices")
         self.table, self.lens, self.starts, self.max_len, self.seqs = table, lens, starts, max_len, seqs
-        self.device = table.device
+        self.index = table.get_device()
         self._c = _Batch(table.data_ptr(), max(table.stride(0), blocks), blocks, lens.data_ptr(),
                          None if starts is None else starts.data_ptr(), seqs, max_len)
         self._ref = ctypes.addressof(self._c)
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current = torch._C._cuda_getDevice
 
 
-class _On:
-    """The device a call runs on made current, if it is not, and its stream."""
+class _Apart:
+    """A call on another stream than the tensors' device's current one, or on
+    a device that is not current: makes the device current for the call, and
+    records on its stream what the call allocated (on the current one)."""
 
-    __slots__ = ("stream", "apart", "_guard")
-
-    def __init__(self, device: torch.device, stream):
-        index = device.index
-        current = torch.cuda.current_device()
-        self._guard = None if index == current else torch.cuda.device(index)
-        own = _raw_stream(index)
+    def __init__(self, index: int, stream):
+        self.index, self.guard, self.other = index, None, None
         if stream is None:
-            self.stream, self.apart = own, None
-            return
-        if hasattr(stream, "cuda_stream"):
+            self.raw = _raw_stream(index)
+        elif hasattr(stream, "cuda_stream"):
             if stream.device.index != index:
                 raise ValueError("stream is on another device than the tensors")
-            self.stream = stream.cuda_stream
+            self.raw = stream.cuda_stream
         else:
-            self.stream = int(stream)
-        self.apart = None
-        if self.stream != own:
-            self.apart = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(self.stream, device=device)
+            self.raw = int(stream)
+        if self.raw != _raw_stream(index):
+            self.other = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(self.raw, device=index)
 
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self
-
-    def __exit__(self, *a):
-        if self._guard is not None:
-            self._guard.__exit__(*a)
-
-    def made(self, t: torch.Tensor) -> torch.Tensor:
-        """A tensor that the call allocated (on the current stream) for use on its stream."""
-        if self.apart is not None:
-            t.record_stream(self.apart)
-        return t
+    def run(self, fn, args, made) -> int:
+        with torch.cuda.device(self.index):
+            status = fn(*args, self.raw)
+            if self.other is not None:
+                for t in made:
+                    t.record_stream(self.other)
+        return status
 
 
-def _heads(t, heads, dim: int, dtype, device, name: str):
-    """(pointer, row stride, heads) of rows [rows][heads][dim] with dense heads."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 3:
-        raise ValueError(f"{name} must be a [rows][heads][{dim}] tensor")
-    shape, stride = t.shape, t.stride()
-    if (heads is not None and shape[1] != heads) or shape[2] != dim:
-        raise ValueError(f"{name} must be [rows][{'heads' if heads is None else heads}][{dim}], got {tuple(shape)}")
-    if t.dtype != dtype:
+def _call(name: str, fn, args, index: int, stream, made=()):
+    if stream is None and index == _current():
+        status = fn(*args, _raw_stream(index))
+    else:
+        status = _Apart(index, stream).run(fn, args, made)
+    if status:
+        raise I2SError(name, status)
+
+
+def _heads(t, heads, dim: int, dtype, index: int, name: str):
+    """(pointer, row stride, heads, rows) of t [rows][heads][dim] with dense
+    heads; heads: their number, or None for any."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if shape[0] and shape[1] and (stride[2] != 1 or (shape[1] > 1 and stride[1] != dim)):
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be a [rows][heads][{dim}] tensor")
+    rows, h, d = t.shape
+    if d != dim or (heads is not None and h != heads):
+        raise ValueError(f"{name} must be [rows][{'heads' if heads is None else heads}][{dim}], got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), h * d, h, rows
+    stride = t.stride()
+    if stride[2] != 1 or (h > 1 and stride[1] != dim):
         raise ValueError(f"{name} must have dense heads (strides [*, {dim}, 1]), got {stride}")
-    width = shape[1] * dim
-    return t.data_ptr(), (stride[0] if shape[0] > 1 else width), shape[1]
+    return t.data_ptr(), (stride[0] if rows > 1 else h * d), h, rows
 
 
-def _type(dtype) -> int:
-    code = _TYPES.get(dtype)
-    if code is None:
-        raise TypeError(f"rows must be float32, float16 or bfloat16, got {dtype}")
+def _like(t, rows: int, heads: int, dim: int) -> torch.Tensor:
+    """A dense tensor of t's shape, type and device."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty((rows, heads, dim), dtype=t.dtype, device=t.device)
+
+
+def _type(t, name: str) -> int:
+    code = _TYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if code is None or t.get_device() < 0:
+        raise TypeError(f"{name} must be a float32, float16 or bfloat16 CUDA (HIP) tensor")
     return code
 
 
-def _same_device(cache: KV8Cache, batch: KV8Batch) -> torch.device:
-    if cache.device != batch.device:
+def _index(cache: KV8Cache, batch: KV8Batch) -> int:
+    if cache.index != batch.index:
         raise ValueError("cache and batch are on different devices")
-    return cache.device
-
-
-def _fail(fn: str, status: int):
-    raise I2SError(fn, status)
+    return cache.index
 
 
 def kv8_append(cache: KV8Cache, batch: KV8Batch, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
     """Quantize rows k, v [rows][heads][dim] into the cache's pages."""
-    device = _same_device(cache, batch)
-    code = _type(k.dtype)
-    kp, ks, _ = _heads(k, cache.heads, cache.dim, k.dtype, device, "k")
-    vp, vs, _ = _heads(v, cache.heads, cache.dim, k.dtype, device, "v")
-    rows = k.shape[0]
-    if v.shape[0] != rows:
+    index = _index(cache, batch)
+    code = _type(k, "k")
+    kp, ks, _, rows = _heads(k, cache.heads, cache.dim, k.dtype, index, "k")
+    vp, vs, _, v_rows = _heads(v, cache.heads, cache.dim, k.dtype, index, "v")
+    if v_rows != rows:
         raise ValueError("k and v have different numbers of rows")
-    with _On(device, stream) as on:
-        st = lib().kv8_append(cache._ref, batch._ref, code, kp, ks, vp, vs, rows, on.stream)
-    if st:
-        _fail("kv8_append", st)
+    _call("kv8_append", lib().kv8_append, (cache._ref, batch._ref, code, kp, ks, vp, vs, rows), index, stream)
 
 
 def kv8_read(cache: KV8Cache, batch: KV8Batch, rows: int, dtype=torch.float32, k=None, v=None, stream=None):
-    """(k, v), each [rows][heads][dim] of `dtype`: the batch's tokens as values.
-    Rows outside the batch's are left as they were in a given k or v, and are
-    undefined in one allocated here."""
-    device = _same_device(cache, batch)
-    with _On(device, stream) as on:
-        shape = (rows, cache.heads, cache.dim)
-        k = on.made(torch.empty(shape, dtype=dtype, device=device)) if k is None else k
-        v = on.made(torch.empty(shape, dtype=dtype, device=device)) if v is None else v
-        if k.shape[0] != rows or v.shape[0] != rows:
-            raise ValueError(f"k and v must have {rows} rows")
-        code = _type(k.dtype)
-        kp, ks, _ = _heads(k, cache.heads, cache.dim, k.dtype, device, "k")
-        vp, vs, _ = _heads(v, cache.heads, cache.dim, k.dtype, device, "v")
-        st = lib().kv8_read(cache._ref, batch._ref, code, kp, ks, vp, vs, rows, on.stream)
-    if st:
-        _fail("kv8_read", st)
+    """(k, v), each [rows][heads][dim] of `dtype` (or k's or v's own): the
+    batch's tokens as values.  Rows outside the batch's are left as they were
+    in a given k or v, and are undefined in one allocated here."""
+    index = _index(cache, batch)
+    heads, dim = cache.heads, cache.dim
+    given = k if k is not None else v
+    dtype = dtype if given is None else given.dtype
+    made = []
+    if k is None:
+        k = torch.empty((rows, heads, dim), dtype=dtype, device=cache.device)
+        kp, ks = k.data_ptr(), heads * dim
+        made.append(k)
+    else:
+        kp, ks, _, n = _heads(k, heads, dim, dtype, index, "k")
+        if n != rows:
+            raise ValueError(f"k must have {rows} rows")
+    if v is None:
+        v = torch.empty_like(k) if made else torch.empty((rows, heads, dim), dtype=dtype, device=cache.device)
+        vp, vs = v.data_ptr(), heads * dim
+        made.append(v)
+    else:
+        vp, vs, _, n = _heads(v, heads, dim, dtype, index, "v")
+        if n != rows:
+            raise ValueError(f"v must have {rows} rows")
+    code = _type(k, "k")
+    _call("kv8_read", lib().kv8_read, (cache._ref, batch._ref, code, kp, ks, vp, vs, rows), index, stream, made)
     return k, v
 
 
@@ -267,37 +278,50 @@ def kv8_attention(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, scale: floa
     of q's shape and type (and lse F32 [rows][q_heads] if lse is a tensor or
     True).  scale: default dim ** -0.5.  Rows outside the batch's are left as
     they were in a given out or lse, and are undefined in one allocated here."""
-    device = _same_device(cache, batch)
-    code = _type(q.dtype)
-    dim = cache.dim
-    qp, qs, q_heads = _heads(q, None, dim, q.dtype, device, "q")
-    rows = q.shape[0]
+    index = _index(cache, batch)
+    code, dim = _type(q, "q"), cache.dim
+    qp, qs, q_heads, rows = _heads(q, None, dim, q.dtype, index, "q")
     L = lib()
-    with _On(device, stream) as on:
-        if out is None:
-            out = on.made(torch.empty((rows, q_heads, dim), dtype=q.dtype, device=device))
-        elif out.shape[0] != rows:
+    made = []
+    if out is None:
+        out = _like(q, rows, q_heads, dim)
+        op, os_ = out.data_ptr(), q_heads * dim
+        made.append(out)
+    else:
+        op, os_, _, n = _heads(out, q_heads, dim, q.dtype, index, "out")
+        if n != rows:
             raise ValueError(f"out must have {rows} rows")
-        op, os_, _ = _heads(out, q_heads, dim, q.dtype, device, "out")
-        lp = None
-        if lse is not None and lse is not False:
-            if lse is True:
-                lse = on.made(torch.empty((rows, q_heads), dtype=torch.float32, device=device))
-            if tuple(_need(lse, torch.float32, 2, "lse").shape) != (rows, q_heads) or not lse.is_contiguous() or lse.device != device:
-                raise ValueError(f"lse must be a contiguous [{rows}][{q_heads}] on {device}")
-            lp = lse.data_ptr()
-        if workspace is None:
-            n = L.kv8_attention_workspace_bytes(cache._ref, batch._ref, q_heads, rows)
-            if n:
-                workspace = on.made(torch.empty(n, dtype=torch.uint8, device=device))
-        elif workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
-        wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-        st = L.kv8_attention(cache._ref, batch._ref, code, qp, qs, q_heads, rows, dim ** -0.5 if scale is None else scale,
-                             1 if causal else 0, window, op, os_, lp, wp, wn, on.stream)
-    if st:
-        _fail("kv8_attention", st)
+    lp = None
+    if lse is not None and lse is not False:
+        if lse is True:
+            lse = torch.empty((rows, q_heads), dtype=torch.float32, device=cache.device)
+            made.append(lse)
+        if tuple(_need(lse, torch.float32, 2, "lse").shape) != (rows, q_heads) or not lse.is_contiguous() or lse.get_device() != index:
+            raise ValueError(f"lse must be a contiguous [{rows}][{q_heads}] on cuda:{index}")
+        lp = lse.data_ptr()
+    wp, wn = None, 0
+    if workspace is None:
+        wn = L.kv8_attention_workspace_bytes(cache._ref, batch._ref, q_heads, rows)
+        if wn:
+            workspace = torch.empty(wn, dtype=torch.uint8, device=cache.device)
+            made.append(workspace)
+            wp = workspace.data_ptr()
+    elif workspace.dtype != torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{index}")
+    else:
+        wp, wn = workspace.data_ptr(), workspace.numel()
+    _call("kv8_attention", L.kv8_attention,
+          (cache._ref, batch._ref, code, qp, qs, q_heads, rows, cache.scale if scale is None else scale, 1 if causal else 0, window,
+           op, os_, lp, wp, wn), index, stream, made)
     return out if lp is None else (out, lse)
+
+
+def _vector(t, n: int, dtype, index: int, name: str):
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != index or t.dim() != 1 or (n >= 0 and t.shape[0] != n) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} [{n if n >= 0 else 'pairs'}] on cuda:{index}")
+    return t.data_ptr()
 
 
 def kv8_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, inv_freq: torch.Tensor, q_weight=None,
@@ -306,38 +330,34 @@ def kv8_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, inv_fr
     [rows][k_heads][dim], RMS-normed per head where a weight F32 [dim] is
     given, then rotated by pos int32 [rows] times inv_freq F32 [pairs].  q_out
     may be q and k_out k."""
-    device, dtype = q.device, q.dtype
-    if not q.is_cuda:
-        raise TypeError("q must be a CUDA (HIP) tensor")
-    code = _type(dtype)
-    rows, dim = q.shape[0], q.shape[-1]
-    qp, qs, q_heads = _heads(q, None, dim, dtype, device, "q")
-    kp, ks, k_heads = _heads(k, None, dim, dtype, device, "k")
-    if k.shape[0] != rows:
+    code, dtype, index = _type(q, "q"), q.dtype, q.get_device()
+    dim = q.shape[-1]
+    qp, qs, q_heads, rows = _heads(q, None, dim, dtype, index, "q")
+    kp, ks, k_heads, k_rows = _heads(k, None, dim, dtype, index, "k")
+    if k_rows != rows:
         raise ValueError("q and k have different numbers of rows")
-    if pos.dtype != torch.int32 or pos.dim() != 1 or pos.shape[0] != rows or not pos.is_contiguous() or pos.device != device:
-        raise ValueError(f"pos must be a contiguous int32 [{rows}] on {device}")
-    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or inv_freq.device != device:
-        raise ValueError(f"inv_freq must be a contiguous float32 [pairs] on {device}")
-    weights = []
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and (w.dtype != torch.float32 or tuple(w.shape) != (dim,) or not w.is_contiguous() or w.device != device):
-            raise ValueError(f"{name} must be a contiguous float32 [{dim}] on {device}")
-        weights.append(None if w is None else w.data_ptr())
-    with _On(device, stream) as on:
-        if q_out is None:
-            q_out = on.made(torch.empty(q.shape, dtype=dtype, device=device))
-        if k_out is None:
-            k_out = on.made(torch.empty(k.shape, dtype=dtype, device=device))
-        if q_out.shape[0] != rows or k_out.shape[0] != rows:
-            raise ValueError(f"q_out and k_out must have {rows} rows")
-        qop, qos, _ = _heads(q_out, q_heads, dim, dtype, device, "q_out")
-        kop, kos, _ = _heads(k_out, k_heads, dim, dtype, device, "k_out")
-        st = lib().kv8_qk_norm_rope(code, rows, dim, qp, qs, q_heads, kp, ks, k_heads, pos.data_ptr(), inv_freq.data_ptr(),
-                                    inv_freq.shape[0], 1 if neighbours else 0, weights[0], weights[1], eps, qop, qos, kop, kos,
-                                    on.stream)
-    if st:
-        _fail("kv8_qk_norm_rope", st)
+    pp, fp = _vector(pos, rows, torch.int32, index, "pos"), _vector(inv_freq, -1, torch.float32, index, "inv_freq")
+    qw, kw = _vector(q_weight, dim, torch.float32, index, "q_weight"), _vector(k_weight, dim, torch.float32, index, "k_weight")
+    made = []
+    if q_out is None:
+        q_out = _like(q, rows, q_heads, dim)
+        qop, qos = q_out.data_ptr(), q_heads * dim
+        made.append(q_out)
+    else:
+        qop, qos, _, n = _heads(q_out, q_heads, dim, dtype, index, "q_out")
+        if n != rows:
+            raise ValueError(f"q_out must have {rows} rows")
+    if k_out is None:
+        k_out = _like(k, rows, k_heads, dim)
+        kop, kos = k_out.data_ptr(), k_heads * dim
+        made.append(k_out)
+    else:
+        kop, kos, _, n = _heads(k_out, k_heads, dim, dtype, index, "k_out")
+        if n != rows:
+            raise ValueError(f"k_out must have {rows} rows")
+    _call("kv8_qk_norm_rope", lib().kv8_qk_norm_rope,
+          (code, rows, dim, qp, qs, q_heads, kp, ks, k_heads, pp, fp, 0 if fp is None else inv_freq.shape[0], 1 if neighbours else 0,
+           qw, kw, eps, qop, qos, kop, kos), index, stream, made)
     return q_out, k_out
 
 

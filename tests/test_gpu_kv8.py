@@ -118,6 +118,7 @@ BATCHES = [
     (2, 128, 64, [300, 64, 129], [300, 64, 64]),
     (1, 256, 16, [50, 17], [33, 17]),
     (2, 48, 256, [600, 256, 3], [400, 1, 3]),
+    (1, 256, 256, [300, 511], [300, 200]),
     (4, 64, 128, [129, 500], [129, 77]),
     (1, 128, 64, [5, 0, 70], [9, 4, 3]),           # more rows than tokens
     (2, 96, 32, [40, 0, -7, 33], [8, 0, 0, 32]),   # empty and negative lengths
