@@ -21,7 +21,7 @@
  *   v       int8 [pages][heads][dim][P]   (tokens innermost: the operand order
  *                                          of the matrix instruction that
  *                                          multiplies by the probabilities)
- *   k_scale, v_scale   F32 [pages][heads]; value = code * scale
+ *   k_scale, v_scale   F32 [pages][heads], finite, >= 0; value = code * scale
  * A sequence's block j (its tokens j*P .. j*P + P-1) is in page table[b][j].
  * An entry outside 0..pages-1 (-1, say) is a hole: appended rows that fall
  * into one are dropped, reading one gives zeros, attention does not see its

@@ -557,6 +557,7 @@ constexpr float kMinScale = 1e-30f;
 constexpr int kTile = 64;          // tokens
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kMaxSplits = 256;
+constexpr int kFewParts = 8;       // that 32 lanes join
 constexpr int kUnits = 256;        // compute units
 
 struct Attend {
@@ -859,18 +860,19 @@ struct Rows {
   }
 
   // Weights of row tile t for the lane's tokens first .. first + 15, and the
-  // running statistics.  edge: some row of the wave does not see them all.
+  // running statistics.  edge: some row of the wave does not see them all, or
+  // some are in a hole.
   __device__ void weigh(int t, const f32x4 (&f)[4], const Scales &s, int first, bool edge, Weights (&w)[kParts]) {
     const float vs = s.hole ? 1.0f : fmaxf(s.vs, kMinScale);
-    const float lvs = s.hole ? -INFINITY : __builtin_amdgcn_logf(vs), rvs = __builtin_amdgcn_rcpf(vs);
-    const float ck = qs[t] * (s.hole ? 0.0f : s.ks);
+    const float lvs = __builtin_amdgcn_logf(vs), rvs = __builtin_amdgcn_rcpf(vs);
+    const float ck = qs[t] * s.ks;
     float e[16];
     auto exponents = [&](float base) {
 #pragma unroll
       for (int k = 0; k < 16; ++k) e[k] = fmaf(f[k / 4][k % 4], ck, base);
       if (edge) {
         const int under = lo[t] - first;
-        const unsigned width = hi[t] > lo[t] ? hi[t] - lo[t] : 0;
+        const unsigned width = !s.hole && hi[t] > lo[t] ? hi[t] - lo[t] : 0;
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           e[k] = static_cast<unsigned>(k - under) < width ? e[k] : -INFINITY;
@@ -1023,7 +1025,7 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_few_k
       kpage = pages.entry(t0 + 2 * kStep + kgroup);
       const int vthen = pages.entry(t0 + 2 * kStep + 16 * g);
       typename R::Weights weights[R::kParts];
-      rows.weigh(0, f, now, t0 + 16 * g, t0 < r.lo || t0 + kTile > r.hi, weights);
+      rows.weigh(0, f, now, t0 + 16 * g, t0 < r.lo || t0 + kTile > r.hi || __any(now.hole), weights);
 #pragma unroll
       for (int d = 0; d < kOut; ++d) {
         if (!kFull && 16 * d >= D) continue;
@@ -1171,7 +1173,7 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_many_
     for (int from = 0; t0 < part.end; t0 += kTile, from ^= 1) {
       begin_round();
       typename R::Weights weights[kRowTiles][R::kParts];
-      const bool edge = t0 < own.lo || t0 + kTile > own.hi;
+      const bool edge = t0 < own.lo || t0 + kTile > own.hi || __any(now.hole);
       f32x4 f[kRowTiles][4];
       i32x4 k[4][kChunks];
 #pragma unroll
@@ -1207,70 +1209,98 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_many_
   }
 }
 
-// Joins the parts of rows that were split.  A row and head is joined by
-// kTeams x 32 lanes, each four components of every kTeams-th part: 8 teams (a
-// workgroup) where there may be many parts, else one.
+// Joins the parts of rows that were split.
+
+// The parts that the row and head at place `at` was cut into.
+__device__ inline int parts_of(const Attend &a, const Span &p, int row, int hq, int block_rows) {
+  const int in_group = (row - p.first) * a.group + hq % a.group, row0 = in_group / block_rows * block_rows;
+  const int rows = p.n * a.group;
+  return range_of(a, p, row0, (row0 + block_rows < rows ? row0 + block_rows : rows) - 1).used;
+}
+
+// Few parts (at most kFewParts): 32 lanes a row and head, four components each.
 // block_rows: rows of the attention's workgroups.
-template <typename T, int kTeams>
-__global__ void __launch_bounds__(kThreads) join_kernel(Attend a, int block_rows) {
-  constexpr int kItems = 8 / kTeams;  // rows and heads of a workgroup
-  __shared__ f32x4 sums[8][KV8_MAX_DIM / 4];
-  const int D = a.c.dim, lane = threadIdx.x & 31, team = kTeams > 1 ? threadIdx.x >> 5 : 0;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kItems + (kTeams > 1 ? 0 : threadIdx.x >> 5);
-  const int64_t each = static_cast<int64_t>(a.s.rows) * a.q_heads;
-  const int row = static_cast<int>((item < each ? item : each - 1) / a.q_heads), hq = static_cast<int>(item - static_cast<int64_t>(row) * a.q_heads);
-  // Rows of one workgroup may lie in two sequences: each wave looks for its
-  // first row's, then (rarely) on from there.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) join_few_kernel(Attend a, int block_rows) {
+  const int each = a.s.rows * a.q_heads, item = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int row = (item < each ? item : each - 1) / a.q_heads, hq = item - row * a.q_heads, D = a.c.dim;
+  // The two rows of a wave may lie in two sequences: the wave looks for the
+  // first's, and the lanes (rarely) on from there.
   Span p = a.s.starts ? find(a.s, __builtin_amdgcn_readfirstlane(row), [](int, int start) { return start; })
                       : span_of(a.s, row / a.s.per_seq);
   if (a.s.starts && p.b >= 0) {
     while (p.b + 1 < a.s.seqs && start_of(a.s, p.b + 1) <= row) p = span_of(a.s, p.b + 1);
   }
-  bool live = item < each && p.b >= 0 && row >= p.first && row < p.first + p.n;
-  Range r = {};
-  if (live) {
-    const int in_group = (row - p.first) * a.group + hq % a.group, row0 = in_group / block_rows * block_rows;
-    const int rows = p.n * a.group;
-    r = range_of(a, p, row0, (row0 + block_rows < rows ? row0 + block_rows : rows) - 1);
-    live = r.used > 1;
-  }
-  if (kTeams > 1 && !live) return;  // the same for the whole workgroup
-  const int used = live ? r.used : 0;
-  const float *ml = a.ml + 2 * item, *acc = a.acc + item * D;
-  // The largest maximum and the denominator, by the team's lanes.
+  const bool live = item < each && p.b >= 0 && row >= p.first && row < p.first + p.n;
+  const int used = live ? parts_of(a, p, row, hq, block_rows) : 0;
+  if (used <= 1) return;
+  const float *ml = a.ml + 2 * static_cast<int64_t>(item), *acc = a.acc + static_cast<int64_t>(item) * D;
+  f32x2 v[kFewParts];
   float now = kNoMax, l = 0.0f;
-  for (int k = lane; k < used; k += 32) now = fmaxf(now, ml[2 * k * each]);
 #pragma unroll
-  for (int k = 1; k < 32; k *= 2) now = fmaxf(now, __shfl_xor(now, k));
-  for (int k = lane; k < used; k += 32) {
-    const f32x2 v = *reinterpret_cast<const f32x2 *>(ml + 2 * k * each);
-    l = fmaf(__builtin_amdgcn_exp2f(v[0] - now), v[1], l);
+  for (int k = 0; k < kFewParts; ++k) {
+    v[k] = f32x2{kNoMax, 0.0f};
+    if (k < used) v[k] = *reinterpret_cast<const f32x2 *>(ml + 2 * k * static_cast<int64_t>(each));
+    now = fmaxf(now, v[k][0]);
   }
 #pragma unroll
-  for (int k = 1; k < 32; k *= 2) l += __shfl_xor(l, k);
+  for (int k = 0; k < kFewParts; ++k) {
+    v[k][0] = __builtin_amdgcn_exp2f(v[k][0] - now);
+    l = fmaf(v[k][0], v[k][1], l);
+  }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   T *out = static_cast<T *>(a.out) + row * a.out_stride + static_cast<int64_t>(hq) * D;
   for (int c = lane; c < D / 4; c += 32) {
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int k = team; k < used; k += kTeams)
-      o += __builtin_amdgcn_exp2f(ml[2 * k * each] - now) * *reinterpret_cast<const f32x4 *>(acc + k * each * D + 4 * c);
-    if (kTeams > 1) {
-      sums[team][c] = o;
-    } else if (live) {
-      store4(out + 4 * c, o * inv);
-    }
-  }
-  if (kTeams > 1) {
-    __syncthreads();
-    for (int c = threadIdx.x; c < D / 4; c += kThreads) {
-      f32x4 o = sums[0][c];
 #pragma unroll
-      for (int k = 1; k < kTeams; ++k) o += sums[k][c];
-      store4(out + 4 * c, o * inv);
-    }
+    for (int k = 0; k < kFewParts; ++k)
+      if (k < used) o += v[k][0] * *reinterpret_cast<const f32x4 *>(acc + k * static_cast<int64_t>(each) * D + 4 * c);
+    store4(out + 4 * c, o * inv);
   }
-  if (a.lse && live && lane == 0 && team == 0) a.lse[item] = l == 0.0f ? -INFINITY : kLn2 * (now + log2f(l));
+  if (a.lse && lane == 0) a.lse[item] = l == 0.0f ? -INFINITY : kLn2 * (now + log2f(l));
+}
+
+// Many parts: a workgroup a row and head; its threads hold the parts' weights,
+// and eight groups of 32 lanes each sum every eighth part.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) join_many_kernel(Attend a, int block_rows) {
+  static_assert(kMaxSplits == kThreads, "a thread holds one part's weight");
+  __shared__ f32x4 sums[8][KV8_MAX_DIM / 4];
+  __shared__ float weight[kMaxSplits], red[4], sl[4];
+  const int row = blockIdx.x, hq = blockIdx.y, tid = threadIdx.x, D = a.c.dim;
+  const Span p = a.s.starts ? find(a.s, row, [](int, int start) { return start; }) : span_of(a.s, row / a.s.per_seq);
+  if (p.b < 0 || row >= p.first + p.n) return;
+  const int used = parts_of(a, p, row, hq, block_rows);
+  if (used <= 1) return;
+  const int64_t each = static_cast<int64_t>(a.s.rows) * a.q_heads, at = static_cast<int64_t>(row) * a.q_heads + hq;
+  const f32x2 v = tid < used ? *reinterpret_cast<const f32x2 *>(a.ml + 2 * (tid * each + at)) : f32x2{kNoMax, 0.0f};
+  float now = wave_max(v[0]);
+  if ((tid & 63) == 0) red[tid >> 6] = now;
+  __syncthreads();
+  now = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  weight[tid] = __builtin_amdgcn_exp2f(v[0] - now);
+  float l = weight[tid] * v[1];
+#pragma unroll
+  for (int k = 1; k < 64; k *= 2) l += __shfl_xor(l, k);
+  if ((tid & 63) == 0) sl[tid >> 6] = l;
+  __syncthreads();
+  l = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+  const int team = tid >> 5;
+  for (int c = tid & 31; c < D / 4; c += 32) {
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int k = team; k < used; k += 8) o += weight[k] * *reinterpret_cast<const f32x4 *>(a.acc + (k * each + at) * D + 4 * c);
+    sums[team][c] = o;
+  }
+  __syncthreads();
+  if (tid < D / 4) {
+    f32x4 o = sums[0][tid];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) o += sums[k][tid];
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    store4(static_cast<T *>(a.out) + row * a.out_stride + static_cast<int64_t>(hq) * D + 4 * tid, o * inv);
+  }
+  if (a.lse && tid == 0) a.lse[at] = l == 0.0f ? -INFINITY : kLn2 * (now + log2f(l));
 }
 
 // ---------------------------------------------------------------------------
@@ -1482,7 +1512,7 @@ int check_attention(const kv8_cache *cache, const kv8_batch *batch, int type, in
                     Batch &s) {
   if (const int st = check_batch(cache, batch, type, rows, c, s)) return st;
   if (q_heads < 1 || q_heads % c.heads) return I2S_EINVAL;
-  if (q_heads > 65535 || rows * (q_heads / c.heads) > kMaxRows ||
+  if (q_heads > 65535 || rows * (q_heads / c.heads) > kMaxRows - 4 * KV8_MAX_PAGE ||
       (static_cast<int64_t>(s.blocks) << c.lp) > kMaxRows - 4 * KV8_MAX_PAGE)
     return I2S_ERANGE;
   return I2S_OK;
@@ -1612,11 +1642,10 @@ extern "C" int kv8_attention(const kv8_cache *cache, const kv8_batch *batch, int
                    : a.c.dim < 128 ? launch_attention<T, 2, false>(p, a, on)
                                    : launch_attention<T, 4, false>(p, a, on);
     if (st || p.splits == 1) return st;
-    const int64_t items = rows * q_heads;
-    if (p.splits > 8) {
-      join_kernel<T, 8><<<static_cast<unsigned>(items), kThreads, 0, on>>>(a, p.block_rows);
+    if (p.splits > kFewParts) {
+      join_many_kernel<T><<<dim3(static_cast<unsigned>(rows), a.q_heads), kThreads, 0, on>>>(a, p.block_rows);
     } else {
-      join_kernel<T, 1><<<static_cast<unsigned>((items + 7) / 8), kThreads, 0, on>>>(a, p.block_rows);
+      join_few_kernel<T><<<static_cast<unsigned>((rows * q_heads + 7) / 8), kThreads, 0, on>>>(a, p.block_rows);
     }
     return hip_status();
   });

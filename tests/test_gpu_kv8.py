@@ -321,6 +321,53 @@ def test_attention_strides_and_shared_pages():
     assert (o[:, :4] == 3).all() and (o[:, 516:] == 3).all()
 
 
+@pytest.mark.parametrize("seqs", [63, 64, 65, 700])
+def test_many_sequences(seqs):
+    """Batches on both sides of the one-load search, with sequences that bring
+    no rows, at the front, between and at the end."""
+    rng = np.random.default_rng(seqs)
+    news = rng.integers(0, 4, size=seqs) * (rng.random(seqs) < 0.7)
+    news[:2] = news[-3:] = 0
+    news[7] = 40
+    lens = news + rng.integers(0, 60, size=seqs)
+    w = World(seqs, 1, 32, 16, lens, news, lead=2)
+    rows = w.rows + 5
+    k, v = w.values(rows, F32), w.values(rows, F32)
+    w.ref.append(k, v)
+    kv8.kv8_append(w.cache, w.batch, dev(k), dev(v))
+    w.same_cache()
+    got = [torch.full((rows, 1, 32), 9.0, device=DEV) for _ in range(2)]
+    kv8.kv8_read(w.cache, w.batch, rows, k=got[0], v=got[1])
+    for g, ref in zip(got, w.ref.read(rows)):
+        assert np.array_equal(bits(host(g)), bits(np.where(np.isnan(ref), np.float32(9.0), ref)))
+    check_attention(w, 3, F32, tag=f"{seqs} sequences")
+    check_attention(w, 40, BF16, tag=f"{seqs} sequences, wide group")
+
+
+def test_attention_with_a_wrong_bound_of_the_lengths():
+    """max_len only steers the split: lengths past it, and tables far longer
+    than any length, give the same values."""
+    w = World(61, 2, 128, 64, [2600, 40], [1, 1], blocks=70)
+    for bound in (1, 100, 0, 4000):
+        w.batch = kv8.KV8Batch(w.batch.table, w.batch.lens, w.batch.starts, max_len=bound)
+        check_attention(w, 6, F32, tag=f"max_len={bound}")
+
+
+def test_attention_rows_before_holes_only():
+    """Rows that see nothing but holes give zeros, whatever their queries."""
+    w = World(62, 2, 64, 16, [40, 33], [3, 2])
+    w.ref.table[0] = -1
+    w.batch.table.copy_(dev(w.ref.table))
+    q = w.values(w.rows, F32, heads=8)
+    q[1, 2, 3], q[4, 1, 0] = np.nan, np.inf
+    out, lse = kv8.kv8_attention(w.cache, w.batch, dev(q), lse=True)
+    o, s = host(out), host(lse)
+    assert not o[:3].any() and np.isneginf(s[:3]).all()
+    bad = np.zeros((5, 8), bool)
+    bad[4, 1] = True
+    assert np.isnan(o[bad]).all() and np.isnan(s[bad]).all() and np.isfinite(o[3:][~bad[3:]]).all()
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_attention_bad_queries_stay_in_their_rows(dtype):
     w = World(15, 2, 128, 64, [200, 90], [2, 20])
