@@ -46,7 +46,9 @@ dequantizing epilogue (two launches); weights quantized once beforehand.
 --workload decode_layer times one Qwen2-1.5B decoder layer's seven ternary
 projections at N = 1 instead (q/k/v grouped with their F32 biases, o,
 gate/up grouped, down: four launches), rotating over 28 layers of weights
-(327.5 MB), beside the same projections as seven separate calls.
+(327.5 MB), beside the same projections as seven separate calls, and (under
+"with_attention") with what lies between q/k/v and o: position rotation,
+append to the layer's int8 K/V cache, attention over 4096 cached tokens.
 
 --workload layer_sweep times each of the seven projections on its own at
 N = 1 and at N = 64 (fourteen i2s_mul_mat calls per step, each weight
@@ -266,13 +268,16 @@ LAYER_PROJ = ("q", "k", "v", "o", "gate", "up", "down")
 LAYERS = 28
 
 
+LAYER_CONTEXT = 4096  # cached tokens of the layer's attention
+
+
 def bench_layer(args, torch, i2s):
     """One Qwen2-1.5B decoder layer's seven ternary projections at decode time
     (N = 1) per step, weights rotating over 28 layers (327.5 MB, beyond the
     Infinity Cache): grouped as q/k/v (one launch, F32 biases), o, gate/up
     (one launch), down -- four launches -- and, for comparison, as seven
     separate calls."""
-    from ternary_weight_integer_amd import workloads
+    from ternary_weight_integer_amd import kv8, workloads
     dev = torch.device("cuda:0")
     case = workloads.decode_layer_case(N=1)
     shp = workloads.QWEN2_1P5B_PROJ
@@ -305,6 +310,37 @@ def bench_layer(args, torch, i2s):
         i2s.i2s_mul_mat_group([(lw["gate"], 8960), (lw["up"], 8960)], 1536, xa, workspace=ws,
                               ys=[y["gate"], y["up"]])
 
+    # The attention of a layer: a cache of 4096 tokens a layer, its last token
+    # this step's.
+    heads, kv_heads, width, page = 12, 2, 128, 64
+    pages = LAYER_CONTEXT // page
+    caches = [kv8.new_cache(pages, kv_heads, width, page, device=dev) for _ in range(LAYERS)]
+    batch = kv8.KV8Batch(torch.arange(pages, dtype=torch.int32, device=dev).view(1, pages),
+                         torch.tensor([LAYER_CONTEXT], dtype=torch.int32, device=dev), max_len=LAYER_CONTEXT)
+    whole = kv8.KV8Batch(batch.table, batch.lens, torch.tensor([0, LAYER_CONTEXT], dtype=torch.int32, device=dev))
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(0)
+    kv = [torch.randn((LAYER_CONTEXT, kv_heads, width), generator=gen, device=dev) for _ in range(2)]
+    for c in caches:
+        kv8.kv8_append(c, whole, *kv)
+    pos = torch.tensor([LAYER_CONTEXT - 1], dtype=torch.int32, device=dev)
+    freq = (1e6 ** (-torch.arange(0, width, 2, dtype=torch.float64, device=dev) / width)).float()
+    qr, kr, att = (torch.empty((1, h, width), device=dev) for h in (heads, kv_heads, heads))
+    attention_ws = torch.empty(max(1, kv8.kv8_attention_workspace_bytes(caches[0], batch, heads, 1)), dtype=torch.uint8,
+                               device=dev)
+
+    def attended(i, out=y2):
+        lw, cache = layers[i % LAYERS], caches[i % LAYERS]
+        i2s.i2s_mul_mat_group([(lw["q"], 1536), (lw["k"], 256), (lw["v"], 256)], 1536, xh,
+                              biases=[bias["q"], bias["k"], bias["v"]], workspace=ws, ys=[out["q"], out["k"], out["v"]])
+        kv8.kv8_qk_norm_rope(out["q"].view(1, heads, width), out["k"].view(1, kv_heads, width), pos, freq, q_out=qr, k_out=kr)
+        kv8.kv8_append(cache, batch, kr, out["v"].view(1, kv_heads, width))
+        kv8.kv8_attention(cache, batch, qr, out=att, workspace=attention_ws)
+        i2s.i2s_mul_mat(lw["o"], 1536, 1536, att.view(1, 1536), workspace=ws, y=out["o"])
+        i2s.i2s_mul_mat_group([(lw["gate"], 8960), (lw["up"], 8960)], 1536, xa, workspace=ws,
+                              ys=[out["gate"], out["up"]])
+        i2s.i2s_mul_mat(lw["down"], 1536, 8960, xf, workspace=ws, y=out["down"])
+
     for i in range(args.warmup):
         grouped(i)
         separate(i)
@@ -327,7 +363,10 @@ def bench_layer(args, torch, i2s):
     g2 = graph_of(lambda: [separate(i) for i in range(K_steps)], torch)
     n_kern = 256
     g3 = graph_of(lambda: [gate_up(i) for i in range(n_kern)], torch)
-    ev = [torch.cuda.Event(enable_timing=True) for _ in range(4)]
+    for i in range(args.warmup):
+        attended(i)
+    g4 = graph_of(lambda: [attended(i) for i in range(K_steps)], torch)
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(5)]
     torch.cuda.synchronize()
     t0 = time.perf_counter()
     ev[0].record()
@@ -337,10 +376,13 @@ def bench_layer(args, torch, i2s):
     ev[2].record()
     g3.replay()
     ev[3].record()
+    g4.replay()
+    ev[4].record()
     torch.cuda.synchronize()
     wall = time.perf_counter() - t0
     step_ms = ev[0].elapsed_time(ev[1]) / K_steps
     sep_ms = ev[1].elapsed_time(ev[2]) / K_steps
+    attended_ms = ev[3].elapsed_time(ev[4]) / K_steps
     kern_us = ev[2].elapsed_time(ev[3]) * 1e3 / n_kern
     alg = 2 * 8960 * 1536 // 4 + 4 * 1536 + 2 * 4 * 8960 + 8   # gate+up weights, x, outputs, two scales
     achieved = alg / (kern_us * 1e-6) / 1e9
@@ -362,6 +404,9 @@ def bench_layer(args, torch, i2s):
                    "timing": "hip_graph"},
         "separate_calls": {"launches_per_step": 7, "ms_per_step": round(sep_ms, 6),
                            "value": round(wbytes / (sep_ms * 1e-3) / 1e9, 3)},
+        "with_attention": {"context": LAYER_CONTEXT, "ms_per_step": round(attended_ms, 6),
+                           "attention_ms": round(attended_ms - step_ms, 6),
+                           "cache_bytes": 2 * LAYER_CONTEXT * kv_heads * width},
         "int8_tops": round(2 * (wbytes * 4) / (step_ms * 1e-3) / 1e12, 4),
         "wall_s": round(wall, 4),
         "roofline": {"bound": "hbm", "achieved": round(achieved, 2), "peak": HBM_PEAK_GBS, "unit": "GB/s",
