@@ -10,6 +10,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -76,12 +77,30 @@ __device__ inline int code_of(float x) {
 }
 
 // ---------------------------------------------------------------------------
+// Division of non-negative ints by a divisor that the host knows: its
+// reciprocal to 32 bits past the divisor's own, rounded up (exact for 31-bit
+// dividends), a multiplication where the hardware has none for '/'.
+struct Divisor {
+  uint32_t by, mul, shift;
+
+  Divisor() = default;
+  explicit Divisor(int d) : by(static_cast<uint32_t>(d)), mul(0), shift(0) {
+    while ((uint64_t{1} << shift) < by) ++shift;
+    // ceil(2^(31 + shift) / by) < 2^32: by > 2^(shift - 1)
+    mul = static_cast<uint32_t>(((uint64_t{1} << (31 + shift)) + by - 1) / by);
+  }
+  __device__ int of(int n) const {
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> 31 >> shift);
+  }
+};
+
 // The batch on the device.
 
 struct Batch {
   const int32_t *table, *lens, *starts;
   int64_t table_stride;
   int blocks, seqs, rows, per_seq;  // per_seq: rows of each sequence where starts is NULL
+  Divisor slots_each;               // page slots of a sequence then
 };
 
 struct Span {
@@ -156,8 +175,8 @@ __device__ inline int page_of(const Batch &s, int b, int64_t j, int pages) {
 __device__ inline bool slot_of(const Batch &s, int lp, int x, Span &p, int64_t &j) {
   int rel;
   if (!s.starts) {
-    const int per = ((s.per_seq + (1 << lp) - 2) >> lp) + 1, b = x / per;
-    rel = x - b * per;
+    const int b = s.slots_each.of(x);
+    rel = x - b * static_cast<int>(s.slots_each.by);
     if (b >= s.seqs) return false;
     p = span_of(s, b);
   } else {
@@ -175,6 +194,7 @@ struct Cache {
   int8_t *k, *v;
   float *k_scale, *v_scale;
   int pages, heads, dim, lp;
+  Divisor by_heads;
 };
 
 // ---------------------------------------------------------------------------
@@ -255,8 +275,8 @@ __device__ inline bool item_of(const Cache &c, const Batch &s, int64_t index, It
   it.n = it.ahead = 0;
   it.page = -1;
   it.value = index & 1;
-  const int slot = static_cast<int>((index >> 1) / c.heads);
-  it.h = static_cast<int>((index >> 1) - static_cast<int64_t>(slot) * c.heads);
+  const int place = static_cast<int>(index >> 1), slot = c.by_heads.of(place);
+  it.h = place - slot * c.heads;
   Span p;
   int64_t j;
   if (!slot_of(s, c.lp, slot, p, j)) return false;
@@ -566,9 +586,11 @@ struct Attend {
   const void *q;
   void *out;
   float *lse, *acc, *ml;  // acc [splits][rows * q_heads][dim], ml [splits][rows * q_heads][2]
-  int64_t q_stride, out_stride, window;
+  int64_t q_stride, out_stride;
   float scale;  // times log2 e
+  int window;
   int q_heads, group, causal, splits;
+  Divisor by_group, by_splits, by_round, by_each, by_heads, by_per_seq;  // by_each: workgroups of a sequence, starts NULL
   int blocks, round;  // workgroups along the rows of one head and part, and those that fill the compute units once
 };
 
@@ -596,19 +618,17 @@ constexpr int kMinPart = 8;  // token tiles of a part: shorter ones do not pay f
 __device__ inline int clamp_int(int64_t v, int top) { return v < 0 ? 0 : v < top ? static_cast<int>(v) : top; }
 
 __device__ inline Range range_of(const Attend &a, const Span &p, int first_row, int last_row) {
-  const int64_t ahead = static_cast<int64_t>(p.len) - p.n;
-  const int64_t p0 = ahead + first_row / a.group, p1 = ahead + last_row / a.group;
-  const int64_t held = static_cast<int64_t>(a.s.blocks) << a.c.lp;
-  const int top = held < p.len ? static_cast<int>(held) : p.len;
+  const int ahead = p.len - p.n, p0 = ahead + a.by_group.of(first_row), p1 = ahead + a.by_group.of(last_row);
+  const int held = a.s.blocks << a.c.lp, top = held < p.len ? held : p.len;
   Range r;
-  r.hi = a.causal ? clamp_int(p0 + 1, top) : top;
-  r.end = a.causal ? clamp_int(p1 + 1, top) : top;
-  r.lo = a.window > 0 ? clamp_int(p1 - a.window + 1, top) : 0;
-  r.begin = (a.window > 0 ? clamp_int(p0 - a.window + 1, top) : 0) & ~(kTile - 1);
+  r.hi = a.causal ? clamp_int(static_cast<int64_t>(p0) + 1, top) : top;
+  r.end = a.causal ? clamp_int(static_cast<int64_t>(p1) + 1, top) : top;
+  r.lo = a.window > 0 ? clamp_int(static_cast<int64_t>(p1) - a.window + 1, top) : 0;
+  r.begin = (a.window > 0 ? clamp_int(static_cast<int64_t>(p0) - a.window + 1, top) : 0) & ~(kTile - 1);
   const int tiles = r.end > r.begin ? (r.end - r.begin + kTile - 1) / kTile : 0;
-  r.part = (tiles + a.splits - 1) / a.splits;
+  r.part = a.by_splits.of(tiles + a.splits - 1);
   if (r.part < kMinPart) r.part = kMinPart;
-  r.used = (tiles + r.part - 1) / r.part;
+  r.used = r.part == kMinPart ? (tiles + kMinPart - 1) / kMinPart : (tiles + r.part - 1) / r.part;
   return r;
 }
 
@@ -659,17 +679,17 @@ struct Place {
 };
 
 __device__ inline bool place_of(const Attend &a, int block_rows, Place &w) {
-  const int rest = blockIdx.x / a.c.heads, G = a.group;
+  const int rest = a.c.by_heads.of(blockIdx.x), G = a.group;
   w.h = blockIdx.x - rest * a.c.heads;
-  int x = rest / a.splits;
+  int x = a.by_splits.of(rest);
   w.split = rest - x * a.splits;
-  const int turn = x / a.round;
+  const int turn = a.by_round.of(x);
   if ((turn & 1) && (turn + 1) * a.round <= a.blocks) x = (2 * turn + 1) * a.round - 1 - x;
   x = a.blocks - 1 - x;
   int rel;
   if (!a.s.starts) {
-    const int per = (a.s.per_seq * G + block_rows - 1) / block_rows, b = x / per;
-    rel = x - b * per;
+    const int b = a.by_each.of(x);
+    rel = x - b * static_cast<int>(a.by_each.by);
     w.p = span_of(a.s, b);
   } else {
     auto key = [&](int i, int start) { return start * G / block_rows + i; };
@@ -763,12 +783,12 @@ struct Rows {
     for (int t = 0; t < kRowTiles; ++t) {
       const int row = row0 + 16 * t + n;
       const bool live = row < w.rows;
-      const int i = live ? row / a.group : 0;
-      const int64_t pos = static_cast<int64_t>(w.p.len) - w.p.n + i;
+      const int i = live ? a.by_group.of(row) : 0;
+      const int pos = w.p.len - w.p.n + i;
       row_of[t] = live ? w.p.first + i : -1;
       head_of[t] = w.h * a.group + (live ? row - i * a.group : 0);
-      hi[t] = !live ? 0 : a.causal ? clamp_int(pos + 1, end) : end;
-      lo[t] = a.window > 0 ? clamp_int(pos - a.window + 1, end) : 0;
+      hi[t] = !live ? 0 : a.causal ? clamp_int(static_cast<int64_t>(pos) + 1, end) : end;
+      lo[t] = a.window > 0 ? clamp_int(static_cast<int64_t>(pos) - a.window + 1, end) : 0;
       qs[t] = 0.0f;
       m[t] = kNoMax;
       l[t] = 0.0f;
@@ -866,33 +886,33 @@ struct Rows {
     const float vs = s.hole ? 1.0f : fmaxf(s.vs, kMinScale);
     const float lvs = __builtin_amdgcn_logf(vs), rvs = __builtin_amdgcn_rcpf(vs);
     const float ck = qs[t] * s.ks;
+    // Taken off the exponents: the running maximum, nothing while there is none.
+    const bool unset = m[t] == kNoMax;
+    const float off = unset ? 0.0f : m[t];
     float e[16];
-    auto exponents = [&](float base) {
 #pragma unroll
-      for (int k = 0; k < 16; ++k) e[k] = fmaf(f[k / 4][k % 4], ck, base);
-      if (edge) {
-        const int under = lo[t] - first;
-        const unsigned width = !s.hole && hi[t] > lo[t] ? hi[t] - lo[t] : 0;
+    for (int k = 0; k < 16; ++k) e[k] = fmaf(f[k / 4][k % 4], ck, lvs - off);
+    if (edge) {
+      const int under = lo[t] - first;
+      const unsigned width = !s.hole && hi[t] > lo[t] ? hi[t] - lo[t] : 0;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          e[k] = static_cast<unsigned>(k - under) < width ? e[k] : -INFINITY;
-          asm volatile("" : "+v"(e[k]));  // keeps this a branch: few tiles take it
-        }
+      for (int k = 0; k < 16; ++k) {
+        e[k] = static_cast<unsigned>(k - under) < width ? e[k] : -INFINITY;
+        asm volatile("" : "+v"(e[k]));  // keeps this a branch: few tiles take it
       }
-      float top = e[0];
+    }
+    float top = e[0];
 #pragma unroll
-      for (int k = 1; k < 16; ++k) top = fmaxf(top, e[k]);
-      return top;
-    };
-    float top = exponents(lvs - m[t]);
-    if (__any(top > kHeadroom)) {
-      top = over_lanes_max(exponents(lvs)) - kHeadroom;
-      const float now = fmaxf(m[t], top), shrink = __builtin_amdgcn_exp2f(m[t] - now);
+    for (int k = 1; k < 16; ++k) top = fmaxf(top, e[k]);
+    if (__any(top > (unset ? -FLT_MAX : kHeadroom))) {
+      top = over_lanes_max(top) + off - kHeadroom;
+      const float now = fmaxf(m[t], top), shrink = __builtin_amdgcn_exp2f(m[t] - now);  // a row that has seen nothing stays unset
       m[t] = now;
       l[t] *= shrink;
 #pragma unroll
       for (int d = 0; d < kOut; ++d) acc[t][d] *= shrink;
-      exponents(lvs - now);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) e[k] = e[k] == -INFINITY ? e[k] : fmaf(f[k / 4][k % 4], ck, lvs - now);
     }
     float sum = 0.0f;
 #pragma unroll
@@ -1013,7 +1033,7 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_few_k
     __builtin_amdgcn_sched_barrier(0);
     rows.set_queries();
 
-    for (; t0 < part.end; t0 += kStep) {
+    while (true) {
       const Scales now = next;
       f32x4 f[4];
 #pragma unroll
@@ -1032,7 +1052,9 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_few_k
 #pragma unroll
         for (int k = 0; k < 2; ++k) rows.add(0, d, k, codes_to_f16(vc[d][2 * k], vc[d][2 * k + 1]), weights);
       }
-      load_v(t0 + kStep, vpage);
+      t0 += kStep;
+      if (t0 >= part.end) break;
+      load_v(t0, vpage);
       vpage = vthen;
     }
   }
@@ -1213,7 +1235,8 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_many_
 
 // The parts that the row and head at place `at` was cut into.
 __device__ inline int parts_of(const Attend &a, const Span &p, int row, int hq, int block_rows) {
-  const int in_group = (row - p.first) * a.group + hq % a.group, row0 = in_group / block_rows * block_rows;
+  const int h = a.by_group.of(hq), in_group = (row - p.first) * a.group + hq - h * a.group;
+  const int row0 = in_group & -block_rows;  // a power of two
   const int rows = p.n * a.group;
   return range_of(a, p, row0, (row0 + block_rows < rows ? row0 + block_rows : rows) - 1).used;
 }
@@ -1223,11 +1246,11 @@ __device__ inline int parts_of(const Attend &a, const Span &p, int row, int hq, 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) join_few_kernel(Attend a, int block_rows) {
   const int each = a.s.rows * a.q_heads, item = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int row = (item < each ? item : each - 1) / a.q_heads, hq = item - row * a.q_heads, D = a.c.dim;
+  const int row = a.by_heads.of(item < each ? item : each - 1), hq = item - row * a.q_heads, D = a.c.dim;
   // The two rows of a wave may lie in two sequences: the wave looks for the
   // first's, and the lanes (rarely) on from there.
   Span p = a.s.starts ? find(a.s, __builtin_amdgcn_readfirstlane(row), [](int, int start) { return start; })
-                      : span_of(a.s, row / a.s.per_seq);
+                      : span_of(a.s, a.by_per_seq.of(row));
   if (a.s.starts && p.b >= 0) {
     while (p.b + 1 < a.s.seqs && start_of(a.s, p.b + 1) <= row) p = span_of(a.s, p.b + 1);
   }
@@ -1268,7 +1291,7 @@ __global__ void __launch_bounds__(kThreads) join_many_kernel(Attend a, int block
   __shared__ f32x4 sums[8][KV8_MAX_DIM / 4];
   __shared__ float weight[kMaxSplits], red[4], sl[4];
   const int row = blockIdx.x, hq = blockIdx.y, tid = threadIdx.x, D = a.c.dim;
-  const Span p = a.s.starts ? find(a.s, row, [](int, int start) { return start; }) : span_of(a.s, row / a.s.per_seq);
+  const Span p = a.s.starts ? find(a.s, row, [](int, int start) { return start; }) : span_of(a.s, a.by_per_seq.of(row));
   if (p.b < 0 || row >= p.first + p.n) return;
   const int used = parts_of(a, p, row, hq, block_rows);
   if (used <= 1) return;
@@ -1434,6 +1457,7 @@ int check_batch(const kv8_cache *c, const kv8_batch *b, int type, int64_t rows, 
   dc.heads = c->heads;
   dc.dim = c->dim;
   dc.lp = __builtin_ctz(c->page_tokens);
+  dc.by_heads = Divisor(c->heads);
   db.table = b->table;
   db.lens = b->lens;
   db.starts = b->starts;
@@ -1442,6 +1466,7 @@ int check_batch(const kv8_cache *c, const kv8_batch *b, int type, int64_t rows, 
   db.seqs = static_cast<int>(b->seqs);
   db.rows = static_cast<int>(rows);
   db.per_seq = b->seqs > 0 ? static_cast<int>(rows / b->seqs) : 0;
+  db.slots_each = Divisor(((db.per_seq + c->page_tokens - 2) >> dc.lp) + 1);
   return I2S_OK;
 }
 
@@ -1554,7 +1579,7 @@ extern "C" int kv8_append(const kv8_cache *cache, const kv8_batch *batch, int ty
   const int64_t width = static_cast<int64_t>(c.heads) * c.dim;
   if (bad_rows(k, k_stride, width, value_bytes(type)) || bad_rows(v, v_stride, width, value_bytes(type))) return I2S_EINVAL;
   const Items n(c, s, true);
-  if (n.blocks > 0x7fffffff) return I2S_ERANGE;
+  if (n.blocks > 0x7fffffff || n.items / 2 > 0x7fffffff) return I2S_ERANGE;
   return by_type(type, [&](auto t) {
     typedef decltype(t) T;
     auto launch = [&](auto kernel) {
@@ -1579,7 +1604,7 @@ extern "C" int kv8_read(const kv8_cache *cache, const kv8_batch *batch, int type
   const int64_t width = static_cast<int64_t>(c.heads) * c.dim;
   if (bad_rows(k, k_stride, width, value_bytes(type)) || bad_rows(v, v_stride, width, value_bytes(type))) return I2S_EINVAL;
   const Items n(c, s, false);
-  if (n.blocks > 0x7fffffff) return I2S_ERANGE;
+  if (n.blocks > 0x7fffffff || n.items / 2 > 0x7fffffff) return I2S_ERANGE;
   return by_type(type, [&](auto t) {
     typedef decltype(t) T;
     auto launch = [&](auto kernel) {
@@ -1625,14 +1650,21 @@ extern "C" int kv8_attention(const kv8_cache *cache, const kv8_batch *batch, int
   a.ml = need ? a.acc + static_cast<int64_t>(p.splits) * rows * q_heads * a.c.dim : nullptr;
   a.q_stride = q_stride;
   a.out_stride = out_stride;
-  a.window = window;
+  a.window = window < kMaxRows ? static_cast<int>(window) : 0;  // positions are below kMaxRows
   a.scale = scale * 1.44269504088896341f;
   a.q_heads = static_cast<int>(q_heads);
   a.group = static_cast<int>(q_heads / a.c.heads);
   a.causal = causal != 0;
+  a.by_group = Divisor(a.group);
+  a.by_splits = Divisor(p.splits);
+  a.by_heads = Divisor(a.q_heads);
+  a.by_per_seq = Divisor(a.s.per_seq > 0 ? a.s.per_seq : 1);
+  const int64_t each = (a.s.per_seq * static_cast<int64_t>(a.group) + p.block_rows - 1) / p.block_rows;
+  a.by_each = Divisor(each > 0 ? static_cast<int>(each) : 1);
   a.splits = p.splits;
   a.blocks = static_cast<int>(p.blocks);
   a.round = kUnits / (a.c.heads * p.splits) > 1 ? kUnits / (a.c.heads * p.splits) : 1;
+  a.by_round = Divisor(a.round);
   const hipStream_t on = static_cast<hipStream_t>(stream);
   return by_type(type, [&](auto t) {
     typedef decltype(t) T;
