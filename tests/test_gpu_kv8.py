@@ -444,7 +444,7 @@ def rope_bound(x, ref, pairs, neighbours, weight, dtype):
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("rows,hq,hk,D,pairs", [(1, 12, 2, 128, 64), (1, 1, 1, 16, 8), (5, 3, 1, 64, 32), (33, 28, 4, 128, 32),
                                                (7, 5, 5, 96, 48), (3, 2, 1, 256, 128), (2500, 2, 1, 48, 16), (9, 16, 0, 80, 0),
-                                               (4, 0, 3, 112, 56), (70, 9, 3, 160, 64)])
+                                               (4, 0, 3, 112, 56), (70, 9, 3, 160, 64), (9001, 2, 1, 16, 8), (4100, 3, 2, 64, 32)])
 def test_norm_and_rotation(rows, hq, hk, D, pairs, dtype):
     rng = np.random.default_rng(rows + D)
     q, k = (rounded(rng.normal(0, 1, size=(rows, h, D)), dtype) for h in (hq, hk))
