@@ -591,6 +591,7 @@ struct Attend {
   float scale;  // times log2 e
   int window;
   int q_heads, group, causal, splits;
+  int least;  // token tiles of a part at least
   Divisor by_group, by_splits, by_round, by_each, by_heads, by_per_seq;  // by_each: workgroups of a sequence, starts NULL
   int blocks, round;  // workgroups along the rows of one head and part, and those that fill the compute units once
 };
@@ -614,7 +615,7 @@ struct Range {
   int begin, end, lo, hi, part, used;
 };
 
-constexpr int kMinPart = 8;  // token tiles of a part: shorter ones do not pay for joining
+constexpr int kLeastFew = 8, kLeastMany = 4;  // token tiles of a part: shorter ones do not pay for joining
 
 __device__ inline int clamp_int(int64_t v, int top) { return v < 0 ? 0 : v < top ? static_cast<int>(v) : top; }
 
@@ -628,8 +629,8 @@ __device__ inline Range range_of(const Attend &a, const Span &p, int first_row, 
   r.begin = (a.window > 0 ? clamp_int(static_cast<int64_t>(p0) - a.window + 1, top) : 0) & ~(kTile - 1);
   const int tiles = r.end > r.begin ? (r.end - r.begin + kTile - 1) / kTile : 0;
   r.part = a.by_splits.of(tiles + a.splits - 1);
-  if (r.part < kMinPart) r.part = kMinPart;
-  r.used = r.part == kMinPart ? (tiles + kMinPart - 1) / kMinPart : (tiles + r.part - 1) / r.part;
+  if (r.part < a.least) r.part = a.least;
+  r.used = (tiles + r.part - 1) / r.part;
   return r;
 }
 
@@ -1498,11 +1499,12 @@ struct Items {
 // How an attention call is laid out: 16-row tiles of a wave (0: four waves
 // share one), rows of a workgroup, and into how many parts tokens are cut.
 struct Plan {
-  int row_tiles, block_rows, splits;
+  int row_tiles, block_rows, splits, least;
   int64_t blocks;  // workgroups along the rows
 };
 
-Plan plan_of(const Cache &c, const Batch &s, int64_t max_len, int64_t q_heads) {
+// The workspace is sized without a window, which only takes parts away.
+Plan plan_of(const Cache &c, const Batch &s, int64_t max_len, int64_t q_heads, int64_t window, bool causal) {
   const int64_t group = q_heads / c.heads, rows = s.rows * group / s.seqs;  // of a sequence, on average
   Plan p;
   auto blocks_of = [&](int block_rows) {
@@ -1518,14 +1520,29 @@ Plan plan_of(const Cache &c, const Batch &s, int64_t max_len, int64_t q_heads) {
   }
   p.block_rows = p.row_tiles ? 64 * p.row_tiles : 16;
   p.blocks = blocks_of(p.block_rows);
+  // Tokens that a workgroup may have to walk.
   const int64_t held = static_cast<int64_t>(s.blocks) << c.lp;
   if (max_len <= 0 || max_len > held) max_len = held;
+  if (window > 0) {
+    const int64_t seen = window + kTile + (causal ? p.block_rows / group + 1 : s.rows);
+    if (max_len > seen) max_len = seen;
+  }
   // Up to two least parts are not worth a second launch (777 tokens: 11.0 us
   // whole, 8.7 + 4.5 us in two parts).
-  const int64_t most = max_len <= 2 * kTile * kMinPart ? 1 : (max_len + kTile * kMinPart - 1) / (kTile * kMinPart);
-  int64_t splits = (p.row_tiles ? 5 : 8) * kUnits / (p.blocks * c.heads);
+  p.least = p.row_tiles ? kLeastMany : kLeastFew;
+  int64_t splits = (p.row_tiles ? 3 : 8) * kUnits / (p.blocks * c.heads);
+  const int64_t most = max_len <= 2 * kTile * p.least ? 1 : (max_len + kTile * p.least - 1) / (kTile * p.least);
   if (splits > most) splits = most;
   if (splits > kMaxSplits) splits = kMaxSplits;
+  if (p.row_tiles && splits > 1) {
+    // Many rows are many partial results.  Microseconds: 2 a tile of tokens
+    // (measured alone, 64 rows of 128 F32 components), 5 for the joining
+    // launch, and writing and reading a part of all rows at 4 TB/s.
+    const double walk = 2.0 * static_cast<double>(max_len) / kTile, part = 8e-6 * s.rows * q_heads * c.dim / 4;
+    const int64_t best = static_cast<int64_t>(sqrt(walk / part));
+    if (splits > best) splits = best;
+    if (splits > 1 && walk / splits + 5.0 + part * splits >= walk) splits = 1;
+  }
   p.splits = splits < 1 ? 1 : static_cast<int>(splits);
   return p;
 }
@@ -1623,7 +1640,7 @@ extern "C" size_t kv8_attention_workspace_bytes(const kv8_cache *cache, const kv
   Cache c;
   Batch s;
   if (check_attention(cache, batch, KV8_F32, q_heads, rows, c, s) || rows == 0 || s.seqs == 0) return 0;
-  return workspace_of(plan_of(c, s, batch->max_len, q_heads), c, s, q_heads);
+  return workspace_of(plan_of(c, s, batch->max_len, q_heads, 0, true), c, s, q_heads);
 }
 
 extern "C" int kv8_attention(const kv8_cache *cache, const kv8_batch *batch, int type, const void *q, int64_t q_stride,
@@ -1637,7 +1654,7 @@ extern "C" int kv8_attention(const kv8_cache *cache, const kv8_batch *batch, int
   if (bad_rows(q, q_stride, width, value_bytes(type)) || bad_rows(out, out_stride, width, value_bytes(type)) ||
       !aligned(lse, 4))
     return I2S_EINVAL;
-  const Plan p = plan_of(a.c, a.s, batch->max_len, q_heads);
+  const Plan p = plan_of(a.c, a.s, batch->max_len, q_heads, window, causal != 0);
   if (p.blocks * a.c.heads * p.splits > 0x7fffffff || rows * q_heads > 0x7fffffff) return I2S_ERANGE;
   const size_t need = workspace_of(p, a.c, a.s, q_heads);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return I2S_EWORKSPACE;
@@ -1660,6 +1677,7 @@ extern "C" int kv8_attention(const kv8_cache *cache, const kv8_batch *batch, int
   const int64_t each = (a.s.per_seq * static_cast<int64_t>(a.group) + p.block_rows - 1) / p.block_rows;
   a.by_each = Divisor(each > 0 ? static_cast<int>(each) : 1);
   a.splits = p.splits;
+  a.least = p.least;
   a.blocks = static_cast<int>(p.blocks);
   a.round = kUnits / (a.c.heads * p.splits) > 1 ? kUnits / (a.c.heads * p.splits) : 1;
   a.by_round = Divisor(a.round);
