@@ -1501,50 +1501,71 @@ struct Items {
 struct Plan {
   int row_tiles, block_rows, splits, least;
   int64_t blocks;  // workgroups along the rows
+  double us;       // what it is thought to take
 };
+
+// The plan with row_tiles given.  Microseconds, as measured for 128 F32
+// components: a wave's walk over a tile of 64 tokens takes 1.9 alone (64 rows
+// of a workgroup), 1.2 where four waves take every fourth tile; a full card
+// does one of 16 rows in 1.15e-3, or 1.6e-3 where each wave turns V for itself
+// and 1.05e-3 for two at a time; joining takes 5 and writing and reading a
+// part of all rows at 4 TB/s.
+Plan plan_for(int row_tiles, const Cache &c, const Batch &s, int64_t len, int64_t q_heads) {
+  const int64_t group = q_heads / c.heads;
+  Plan p;
+  p.row_tiles = row_tiles;
+  p.block_rows = row_tiles ? 64 * row_tiles : 16;
+  p.blocks = s.starts ? s.rows * group / p.block_rows + s.seqs
+                      : (s.per_seq * group + p.block_rows - 1) / p.block_rows * s.seqs;
+  // Up to two least parts are not worth a second launch (777 tokens: 11.0 us
+  // whole, 8.7 + 4.5 us in two parts).
+  p.least = row_tiles ? kLeastMany : kLeastFew;
+  int64_t splits = (row_tiles ? 4 : 8) * kUnits / (p.blocks * c.heads);
+  const int64_t most = len <= 2 * kTile * p.least ? 1 : (len + kTile * p.least - 1) / (kTile * p.least);
+  if (splits > most) splits = most;
+  if (splits > kMaxSplits) splits = kMaxSplits;
+  if (splits < 1) splits = 1;
+  const double tiles = static_cast<double>(len) / kTile, walk = tiles * (row_tiles ? 1.9 : 0.3);
+  const double part = 8e-6 * s.rows * q_heads * c.dim / 4;
+  if (splits > 1) {  // many rows are many partial results
+    const int64_t best = static_cast<int64_t>(sqrt(walk / part));
+    if (splits > best) splits = best;
+    if (splits <= 1 || walk / splits + 5.0 + part * splits >= walk) splits = 1;
+  }
+  p.splits = static_cast<int>(splits);
+  const double full = tiles * s.rows * q_heads / 16 * (c.dim + 64) / 192 *
+                      (row_tiles == 0 ? 1.6e-3 : row_tiles == 1 ? 1.15e-3 : 1.05e-3);
+  p.us = (walk / splits > full ? walk / splits : full) + (splits > 1 ? 5.0 + part * splits : 0.0);
+  return p;
+}
 
 // The workspace is sized without a window, which only takes parts away.
 Plan plan_of(const Cache &c, const Batch &s, int64_t max_len, int64_t q_heads, int64_t window, bool causal) {
   const int64_t group = q_heads / c.heads, rows = s.rows * group / s.seqs;  // of a sequence, on average
-  Plan p;
-  auto blocks_of = [&](int block_rows) {
-    return s.starts ? s.rows * group / block_rows + s.seqs : (s.per_seq * group + block_rows - 1) / block_rows * s.seqs;
-  };
-  p.row_tiles = 0;
+  const int64_t held = static_cast<int64_t>(s.blocks) << c.lp;
+  if (max_len <= 0 || max_len > held) max_len = held;
+  // Over 26 calls each of 48 to 128, to 512 and of more rows a sequence, lengths
+  // drawn up to 4096 and beyond, the kernel for few rows took 1.31, 1.28 and 2.10
+  // times (floor + 8 us) in the mean, that for many 1.50, 1.48 and 1.75, the
+  // one of the lower estimate 1.32, 1.28 and 1.70.
+  Plan best = plan_for(0, c, s, max_len, q_heads);
   if (rows > 16) {
     // Two tiles of rows a wave read and turn V half as often, one leaves more
     // workgroups to balance: 16 heads of width 64, prompts of 150 to 5000
     // tokens, 172 against 185 us; 12 heads of width 128, one prompt of 4096
     // tokens in F32 (386 workgroups of two tiles), 176 against 122 us.
-    p.row_tiles = c.dim <= 128 && rows > 64 && blocks_of(128) * c.heads >= 4 * kUnits ? 2 : 1;
+    Plan many = plan_for(2, c, s, max_len, q_heads);
+    if (c.dim > 128 || rows <= 64 || many.blocks * c.heads < 4 * kUnits) many = plan_for(1, c, s, max_len, q_heads);
+    if (many.us < best.us) best = many;
   }
-  p.block_rows = p.row_tiles ? 64 * p.row_tiles : 16;
-  p.blocks = blocks_of(p.block_rows);
-  // Tokens that a workgroup may have to walk.
-  const int64_t held = static_cast<int64_t>(s.blocks) << c.lp;
-  if (max_len <= 0 || max_len > held) max_len = held;
-  if (window > 0) {
-    const int64_t seen = window + kTile + (causal ? p.block_rows / group + 1 : s.rows);
-    if (max_len > seen) max_len = seen;
+  if (window > 0 && best.splits > 1) {  // fewer tokens to walk
+    const int64_t seen = window + kTile + (causal ? best.block_rows / group + 1 : s.rows);
+    if (seen < max_len) {
+      const int splits = plan_for(best.row_tiles, c, s, seen, q_heads).splits;
+      if (splits < best.splits) best.splits = splits;
+    }
   }
-  // Up to two least parts are not worth a second launch (777 tokens: 11.0 us
-  // whole, 8.7 + 4.5 us in two parts).
-  p.least = p.row_tiles ? kLeastMany : kLeastFew;
-  int64_t splits = (p.row_tiles ? 3 : 8) * kUnits / (p.blocks * c.heads);
-  const int64_t most = max_len <= 2 * kTile * p.least ? 1 : (max_len + kTile * p.least - 1) / (kTile * p.least);
-  if (splits > most) splits = most;
-  if (splits > kMaxSplits) splits = kMaxSplits;
-  if (p.row_tiles && splits > 1) {
-    // Many rows are many partial results.  Microseconds: 2 a tile of tokens
-    // (measured alone, 64 rows of 128 F32 components), 5 for the joining
-    // launch, and writing and reading a part of all rows at 4 TB/s.
-    const double walk = 2.0 * static_cast<double>(max_len) / kTile, part = 8e-6 * s.rows * q_heads * c.dim / 4;
-    const int64_t best = static_cast<int64_t>(sqrt(walk / part));
-    if (splits > best) splits = best;
-    if (splits > 1 && walk / splits + 5.0 + part * splits >= walk) splits = 1;
-  }
-  p.splits = splits < 1 ? 1 : static_cast<int>(splits);
-  return p;
+  return best;
 }
 
 // Checks shared by kv8_attention and its workspace's size.
