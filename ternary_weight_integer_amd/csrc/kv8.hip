@@ -201,13 +201,13 @@ struct Cache {
 // Append and read-back.
 //
 // One item is a page slot, a head, and K or V.  A lane works on units of
-// kTokens (8 or 16) tokens x 4 components: 32 neighbouring lanes cover a row of 128 components,
-// so rows are read and written in whole lines, and V's turning (tokens
+// kTokens (8 or 16) tokens x 4 components: 32 neighbouring lanes cover a row of
+// 128 components, so rows are read and written in whole lines, and V's turning (tokens
 // innermost in the page) is 4 x 4 byte transposes within the lane.  A wave has
 // 64 units at a time; an item has as many waves as its units fill, up to the
 // workgroup's 4.
 
-constexpr int kUnitDims = 4, kFewTokens = 4;
+constexpr int kUnitDims = 4, kAppendTokens = 8, kFewTokens = 4;
 
 template <typename T>
 struct Four {
@@ -372,12 +372,15 @@ __device__ inline void append_few(const T *src, int64_t stride, int8_t *codes, f
 }
 
 // Append: the maximum of the item's new values, the page's scale, then the
-// codes.  kOnce: the item's units fill its waves once, and the values stay in
+// codes.  Bound by the chain of lookup, values, maximum and stores: 7 prompts
+// (12163 rows of 2 heads of 128 F32 values, 31 MB) in 15 us, with units of 4, 8
+// or 16 tokens and with V's units dealt to lanes along tokens alike.  kOnce: the item's units fill its waves once, and the values stay in
 // registers between the two; else they are read again (from the cache).
-template <typename T, int kTokens, bool kOnce>
+template <typename T, bool kOnce>
 __global__ void __launch_bounds__(kThreads) append_kernel(Cache c, Batch s, const T *__restrict__ kx, int64_t k_stride,
                                                           const T *__restrict__ vx, int64_t v_stride, int waves,
                                                           int64_t items) {
+  constexpr int kTokens = kAppendTokens;
   __shared__ float red[kThreads / 64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t index = static_cast<int64_t>(blockIdx.x) * (4 / waves) + wave / waves;
@@ -486,7 +489,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Cache c, Batch s, cons
   }
 }
 
-// Read-back, the inverse.
+// Read-back, the inverse.  Bound by memory: 405 MB of codes and BF16 values in
+// 70 to 83 us (4.9 to 5.8 TB/s).
 template <typename T, int kTokens>
 __global__ void __launch_bounds__(kThreads) read_kernel(Cache c, Batch s, T *__restrict__ ko, int64_t k_stride,
                                                         T *__restrict__ vo, int64_t v_stride, int waves, int64_t items) {
@@ -982,7 +986,11 @@ __device__ inline f16x8 codes_to_f16(int low, int high) {
 // joined through shared memory.  Bound by the cache's bytes: a tile's K is
 // loaded while the tile before it is weighted and multiplied by V, its V while
 // its own logits are formed, into the registers that the tile before has just
-// left; the pages are looked up one tile further ahead.
+// left; the pages are looked up one tile further ahead.  64 sequences of 500 to
+// 8000 tokens, 32 query heads over 8 of 128, BF16: 108 us for 559 MB (5.2 TB/s;
+// a read alone reaches 5.4 to 6.4).  A single sequence of 777 tokens takes 8.7
+// to 11 us, latency and the fetch of instructions, one of 65536 tokens and 2
+// heads 11 us (3.1 TB/s).  Eight waves, or two tiles on their way, were slower.
 // kChunks: 64-component chunks of a head, kFull: the head fills them.
 template <typename T, int kChunks, bool kFull>
 __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_few_kernel(Attend a) {
@@ -1097,7 +1105,14 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_few_k
 // quarter of the next tile's operands while the present one is worked on,
 // turns its part of V into f16 (once for the workgroup), and lays both down
 // in shared memory in the order in which lanes take them: 64 lanes x 16
-// bytes, free of bank conflicts.
+// bytes, free of bank conflicts.  Bound by issuing vector instructions (a
+// weight's exponent, sum and f16 parts, the digits' joining) and the matrix
+// products, which a wave does by turns.  A causal prompt of 4096 F32 rows, 12
+// query heads over 2 of 128: 107 to 113 us, 0.47 PFLOP/s of the formula's
+// operations, 1.2 of those of three digits and two parts; vector instructions
+// are active in 55% of the SIMDs' cycles, the matrix units in 32%.  Six BF16
+// prompts of 150 to 5000 tokens, 16 query heads over 4 of 64, a window of 1024:
+// 145 us, 0.46 PFLOP/s; 78% and 18%.
 template <typename T, int kChunks, bool kFull, int kRowTiles>
 __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_many_kernel(Attend a) {
   typedef Rows<T, kChunks, kFull, kRowTiles> R;
@@ -1332,14 +1347,15 @@ __global__ void __launch_bounds__(kThreads) join_many_kernel(Attend a, int block
 // Norm and rotation.  A wave takes one row and a share of its heads, or (few
 // heads) several rows.  A lane holds 32 bytes of a head: the two halves of its
 // pairs (16 bytes at i and 16 at i + pairs), or 32 neighbouring bytes, so a
-// rotation never leaves its lane; only the norm's sum crosses lanes.  Bound by
-// memory: 8192 rows of 40 heads of 128 BF16 values in 35 us (4.7 TB/s).
+// rotation never leaves its lane (and may be in place); only the norm's sum
+// crosses lanes.  Bound by memory: 8192 rows of 40 heads of 128 BF16 values in
+// 34 to 37 us (4.6 TB/s).
 
 constexpr int kMaxTurns = 512;  // angles of a wave
 
 template <typename T, bool kNeighbours>
 __global__ void __launch_bounds__(kThreads)
-    rope_kernel(const T *__restrict__ q, int64_t q_stride, int q_heads, const T *__restrict__ k, int64_t k_stride,
+    rope_kernel(const T *q, int64_t q_stride, int q_heads, const T *k, int64_t k_stride,
                 int k_heads, const int32_t *__restrict__ pos, const float *__restrict__ inv_freq, int pairs,
                 const float *__restrict__ q_weight, const float *__restrict__ k_weight, float eps, T *q_out,
                 int64_t q_out_stride, T *k_out, int64_t k_out_stride, int rows, int dim, int lanes_log, int rows_log,
@@ -1487,7 +1503,7 @@ struct Items {
     // (84 against 91 us for 65536 x 8 x 128 values, BF16), units of 8 make more
     // waves where there are few (5.6 against 6.5 us for 1100 x 2 x 128, F32).
     // Appending holds a unit's values in registers: 8.
-    tokens = append || items << c.lp < (INT64_C(1) << 19) ? 8 : 16;
+    tokens = append ? kAppendTokens : items << c.lp < (INT64_C(1) << 19) ? 8 : 16;
     units = (1 << c.lp) / tokens * (c.dim / kUnitDims);
     waves = units <= 64 ? 1 : units <= 128 ? 2 : 4;
     // A decode step's items are one wave's work.
@@ -1586,13 +1602,12 @@ inline size_t workspace_of(const Plan &p, const Cache &c, const Batch &s, int64_
 template <typename T, int kChunks, bool kFull>
 int launch_attention(const Plan &p, const Attend &a, hipStream_t stream) {
   const unsigned grid = static_cast<unsigned>(p.blocks * a.c.heads * p.splits);
-  constexpr int kMost = kChunks > 2 ? 1 : 2;  // row tiles that fit the registers
   if (p.row_tiles == 0) {
     attention_few_kernel<T, kChunks, kFull><<<grid, kThreads, 0, stream>>>(a);
   } else if (p.row_tiles == 1) {
     attention_many_kernel<T, kChunks, kFull, 1><<<grid, kThreads, 0, stream>>>(a);
-  } else {
-    attention_many_kernel<T, kChunks, kFull, kMost><<<grid, kThreads, 0, stream>>>(a);
+  } else if constexpr (kChunks <= 2) {  // two row tiles fit the registers, see plan_of
+    attention_many_kernel<T, kChunks, kFull, 2><<<grid, kThreads, 0, stream>>>(a);
   }
   return hip_status();
 }
@@ -1623,9 +1638,9 @@ extern "C" int kv8_append(const kv8_cache *cache, const kv8_batch *batch, int ty
           c, s, static_cast<const T *>(k), k_stride, static_cast<const T *>(v), v_stride, n.waves, n.items);
     };
     if (n.units <= 64 * n.waves) {
-      launch(append_kernel<T, 8, true>);
+      launch(append_kernel<T, true>);
     } else {
-      launch(append_kernel<T, 8, false>);
+      launch(append_kernel<T, false>);
     }
     return hip_status();
   });
