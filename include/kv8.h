@@ -101,7 +101,8 @@ typedef struct kv8_batch {
  *   k, v     [rows][heads][dim] of `type`, finite, 16-byte aligned, heads
  *            dense; k_stride, v_stride: elements from row to row, multiples of
  *            16 bytes, >= heads * dim.
- * A page that receives rows must belong to one sequence of the batch alone.
+ * A page that receives rows stands once in the batch's table: in one sequence,
+ * for one block (its contents are undefined otherwise).
  * Errors: I2S_EINVAL (a null or misaligned pointer, an unknown type, a
  * negative size, a stride, starts NULL with rows not a multiple of seqs),
  * I2S_EALIGN (dim, page_tokens), I2S_ERANGE, I2S_EHIP. */

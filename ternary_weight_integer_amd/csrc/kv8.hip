@@ -374,8 +374,9 @@ __device__ inline void append_few(const T *src, int64_t stride, int8_t *codes, f
 // Append: the maximum of the item's new values, the page's scale, then the
 // codes.  Bound by the chain of lookup, values, maximum and stores: 7 prompts
 // (12163 rows of 2 heads of 128 F32 values, 31 MB) in 15 us, with units of 4, 8
-// or 16 tokens and with V's units dealt to lanes along tokens alike.  kOnce: the item's units fill its waves once, and the values stay in
-// registers between the two; else they are read again (from the cache).
+// or 16 tokens and with V's units dealt to lanes along tokens alike.  kOnce:
+// the item's units fill its waves once, and the values stay in registers
+// between the two; else they are read again (from the cache).
 template <typename T, bool kOnce>
 __global__ void __launch_bounds__(kThreads) append_kernel(Cache c, Batch s, const T *__restrict__ kx, int64_t k_stride,
                                                           const T *__restrict__ vx, int64_t v_stride, int waves,

@@ -132,6 +132,8 @@ class KV8Batch:
         seqs, blocks = table.shape
         if blocks > 1 and table.stride(1) != 1:
             raise ValueError("table must have unit innermost stride")
+        if seqs > 1 and table.stride(0) < blocks:
+            raise ValueError(f"table's rows must not overlap, got strides {table.stride()}")
         if lens.shape[0] != seqs or not lens.is_contiguous():
             raise ValueError(f"lens must be a contiguous [{seqs}], got {tuple(lens.shape)}")
         if starts is not None:

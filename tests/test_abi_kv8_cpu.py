@@ -171,6 +171,20 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         kv8.kv8_qk_norm_rope(z((1, 1, 16)), z((1, 1, 16)), z(1, dtype=torch.int32), z(8))
 
 
+def test_binding_refuses_a_table_whose_rows_overlap(monkeypatch):
+    """A broadcast table has a row stride of 0: taken as dense, its rows would
+    be looked for behind its memory."""
+    monkeypatch.setattr(kv8, "_need", lambda t, dtype, dim, name: t)  # the checks of strides, on host tensors
+    lens = torch.zeros(4, dtype=torch.int32)
+    wide = torch.zeros((4, 10), dtype=torch.int32)
+    for table in (wide[:1].expand(4, 10), wide[:1, :1].expand(4, 1), torch.as_strided(wide, (4, 5), (3, 1))):
+        with pytest.raises(ValueError, match="overlap"):
+            kv8.KV8Batch(table, lens)
+    assert kv8.KV8Batch(wide[:, :6], lens)._c.table_stride == 10
+    assert kv8.KV8Batch(wide[:1].expand(1, 10), lens[:1])._c.table_stride == 10
+    assert kv8.KV8Batch(wide[:, :0], lens)._c.blocks == 0
+
+
 def test_page_slots_cover_every_touched_page_once():
     """The kernels' slot arithmetic (key(b) = start(b) / P + 2 b, rows / P + 2
     seqs slots), modelled here: every page that receives rows has one slot of
