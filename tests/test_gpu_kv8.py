@@ -344,6 +344,26 @@ def test_many_sequences(seqs):
     check_attention(w, 40, BF16, tag=f"{seqs} sequences, wide group")
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("heads,D,group,seqs,rows", [(8, 64, 4, 60, 70), (8, 128, 4, 60, 70), (16, 48, 2, 40, 67), (8, 112, 7, 40, 66)])
+def test_attention_of_many_rows(heads, D, group, seqs, rows, dtype):
+    """More workgroups of 128 rows (rows / 128 + 1 of each sequence and head)
+    than four times the compute units: waves of two row tiles, some of which
+    end inside the second, or before it."""
+    rng = np.random.default_rng(seqs + D)
+    news = rng.integers(rows - 40, rows + 20, size=seqs)
+    news[3] = 0
+    assert heads * (int(news.sum()) * group // 128 + seqs) >= 1024
+    w = World(D, heads, D, 32, news + rng.integers(0, 50, size=seqs) * (rng.random(seqs) < 0.5), news, lead=1)
+    check_attention(w, group, dtype, tag="many rows")
+    check_attention(w, group, dtype, window=40, tag="many rows")
+
+
+def test_attention_of_a_very_wide_group():
+    w = World(64, 1, 64, 64, [400, 30], [2, 1])
+    check_attention(w, 1000, F32, tag="1000 heads over one")
+
+
 def test_attention_with_a_wrong_bound_of_the_lengths():
     """max_len only steers the split: lengths past it, and tables far longer
     than any length, give the same values."""
@@ -597,6 +617,30 @@ def test_side_stream_and_raw_handle():
         out = kv8.kv8_attention(w.cache, w.batch, q)
     side.synchronize()
     assert torch.equal(out, want)
+
+
+def test_two_calls_at_once():
+    """Attention of two batches over one cache, and an append to another, on
+    three streams together: each as when it runs alone."""
+    w, x = World(41, 2, 128, 64, [2500, 300, 900], [1, 1, 1]), World(42, 2, 128, 64, [200, 90], [100, 90])
+    one = kv8.KV8Batch(w.batch.table[:1], w.batch.lens[:1].clone(), max_len=2500)
+    q = [dev(w.values(n, F32, heads=12)) for n in (3, 1)]
+    want = [kv8.kv8_attention(w.cache, w.batch, q[0]), kv8.kv8_attention(w.cache, one, q[1])]
+    k, v = x.values(190, F32), x.values(190, F32)
+    x.ref.append(k, v)
+    kd, vd = dev(k), dev(v)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for turn in range(8):
+        with torch.cuda.stream(streams[0]):
+            a = kv8.kv8_attention(w.cache, w.batch, q[0])
+        with torch.cuda.stream(streams[1]):
+            b = kv8.kv8_attention(w.cache, one, q[1])
+        if turn == 0:
+            kv8.kv8_append(x.cache, x.batch, kd, vd, stream=streams[2])
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+    x.same_cache()
 
 
 def test_binding_refusals():
