@@ -5,7 +5,7 @@ with tolerances that the arithmetic gives.
 
 u = 2^-24 below: half a step of F32, relative.  Attention in F32 rows:
   - a query is held as a fixed-point number of 23 bits of its row's largest
-    magnitude: |dq| <= 1.5 steps of max|q| / 8323072 = 3 u max|q|, so an
+    magnitude: |dq| <= 1.5 steps of max|q| / (127 * 65536) = 3 u max|q|, so an
     exponent e is off by at most 3 u spread, spread = |scale| k_scale
     sum|code| max|q| (the oracle gives its maximum over the row);
   - four roundings of partial sums (each at most u spread), and roundings of
