@@ -1265,12 +1265,19 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) join_few_kernel(Attend a, int block_rows) {
   const int each = a.s.rows * a.q_heads, item = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int row = a.by_heads.of(item < each ? item : each - 1), hq = item - row * a.q_heads, D = a.c.dim;
-  // The two rows of a wave may lie in two sequences: the wave looks for the
-  // first's, and the lanes (rarely) on from there.
-  Span p = a.s.starts ? find(a.s, __builtin_amdgcn_readfirstlane(row), [](int, int start) { return start; })
-                      : span_of(a.s, a.by_per_seq.of(row));
-  if (a.s.starts && p.b >= 0) {
-    while (p.b + 1 < a.s.seqs && start_of(a.s, p.b + 1) <= row) p = span_of(a.s, p.b + 1);
+  // A wave's two items may lie in neighbouring rows, and these in two sequences
+  // or the first in front of all: then each row's sequence is looked for.
+  Span p;
+  if (!a.s.starts) {
+    p = span_of(a.s, a.by_per_seq.of(row));
+  } else {
+    auto key = [](int, int start) { return start; };
+    const int first = __builtin_amdgcn_readlane(row, 0), second = __builtin_amdgcn_readlane(row, 32);
+    p = find(a.s, first, key);
+    if (second != first) {
+      const Span other = find(a.s, second, key);
+      if (row == second) p = other;
+    }
   }
   const bool live = item < each && p.b >= 0 && row >= p.first && row < p.first + p.n;
   const int used = live ? parts_of(a, p, row, hq, block_rows) : 0;
