@@ -9,7 +9,10 @@ change from call to call).
 
 Every call runs on the device of its tensors.  `stream` (a torch stream or a
 raw handle; default: that device's current stream) is where the kernels are
-enqueued: outputs and workspaces that a call allocates are recorded on it.
+enqueued, and of whose memory outputs and workspaces that a call allocates are
+taken: work still queued on the current stream cannot be using it.  Outputs are
+recorded on the current stream too, where their user is taken to read them
+(after a wait of its own).
 """
 
 from __future__ import annotations
@@ -155,11 +158,10 @@ _current = torch._C._cuda_getDevice
 
 class _Apart:
     """A call on another stream than the tensors' device's current one, or on
-    a device that is not current: makes the device current for the call, and
-    records on its stream what the call allocated (on the current one)."""
+    a device that is not current."""
 
     def __init__(self, index: int, stream):
-        self.index, self.guard, self.other = index, None, None
+        self.index, self.other = index, None
         if stream is None:
             self.raw = _raw_stream(index)
         elif hasattr(stream, "cuda_stream"):
@@ -169,22 +171,40 @@ class _Apart:
         else:
             self.raw = int(stream)
         if self.raw != _raw_stream(index):
-            self.other = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(self.raw, device=index)
+            if hasattr(stream, "cuda_stream"):
+                self.other = stream
+            elif self.raw:
+                self.other = torch.cuda.ExternalStream(self.raw, device=index)
+            else:
+                self.other = torch.cuda.default_stream(index)
 
-    def run(self, fn, args, made) -> int:
+    def new(self, kept: bool, fn, *args, **kw) -> torch.Tensor:
+        """fn(*args, **kw), a new tensor: of the memory of the call's stream,
+        and recorded on the current one if the caller gets it (kept)."""
+        if self.other is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(self.other):
+            t = fn(*args, **kw)
+        if kept:
+            t.record_stream(torch.cuda.current_stream(self.index))
+        return t
+
+    def run(self, fn, args) -> int:
         with torch.cuda.device(self.index):
-            status = fn(*args, self.raw)
-            if self.other is not None:
-                for t in made:
-                    t.record_stream(self.other)
-        return status
+            return fn(*args, self.raw)
 
 
-def _call(name: str, fn, args, index: int, stream, made=()):
-    if stream is None and index == _current():
-        status = fn(*args, _raw_stream(index))
-    else:
-        status = _Apart(index, stream).run(fn, args, made)
+def _place(index: int, stream):
+    """Where a call runs: None for the current stream of the current device."""
+    return None if stream is None and index == _current() else _Apart(index, stream)
+
+
+def _new(at, kept: bool, fn, *args, **kw) -> torch.Tensor:
+    return fn(*args, **kw) if at is None else at.new(kept, fn, *args, **kw)
+
+
+def _call(name: str, fn, args, index: int, at):
+    status = fn(*args, _raw_stream(index)) if at is None else at.run(fn, args)
     if status:
         raise I2SError(name, status)
 
@@ -237,7 +257,7 @@ def kv8_append(cache: KV8Cache, batch: KV8Batch, k: torch.Tensor, v: torch.Tenso
     vp, vs, _, v_rows = _heads(v, cache.heads, cache.dim, k.dtype, index, "v")
     if v_rows != rows:
         raise ValueError("k and v have different numbers of rows")
-    _call("kv8_append", lib().kv8_append, (cache._ref, batch._ref, code, kp, ks, vp, vs, rows), index, stream)
+    _call("kv8_append", lib().kv8_append, (cache._ref, batch._ref, code, kp, ks, vp, vs, rows), index, _place(index, stream))
 
 
 def kv8_read(cache: KV8Cache, batch: KV8Batch, rows: int, dtype=torch.float32, k=None, v=None, stream=None):
@@ -248,25 +268,23 @@ def kv8_read(cache: KV8Cache, batch: KV8Batch, rows: int, dtype=torch.float32, k
     heads, dim = cache.heads, cache.dim
     given = k if k is not None else v
     dtype = dtype if given is None else given.dtype
-    made = []
+    at = _place(index, stream)
     if k is None:
-        k = torch.empty((rows, heads, dim), dtype=dtype, device=cache.device)
+        k = _new(at, True, torch.empty, (rows, heads, dim), dtype=dtype, device=cache.device)
         kp, ks = k.data_ptr(), heads * dim
-        made.append(k)
     else:
         kp, ks, _, n = _heads(k, heads, dim, dtype, index, "k")
         if n != rows:
             raise ValueError(f"k must have {rows} rows")
     if v is None:
-        v = torch.empty_like(k) if made else torch.empty((rows, heads, dim), dtype=dtype, device=cache.device)
+        v = _new(at, True, torch.empty, (rows, heads, dim), dtype=dtype, device=cache.device)
         vp, vs = v.data_ptr(), heads * dim
-        made.append(v)
     else:
         vp, vs, _, n = _heads(v, heads, dim, dtype, index, "v")
         if n != rows:
             raise ValueError(f"v must have {rows} rows")
     code = _type(k, "k")
-    _call("kv8_read", lib().kv8_read, (cache._ref, batch._ref, code, kp, ks, vp, vs, rows), index, stream, made)
+    _call("kv8_read", lib().kv8_read, (cache._ref, batch._ref, code, kp, ks, vp, vs, rows), index, at)
     return k, v
 
 
@@ -283,12 +301,10 @@ def kv8_attention(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, scale: floa
     index = _index(cache, batch)
     code, dim = _type(q, "q"), cache.dim
     qp, qs, q_heads, rows = _heads(q, None, dim, q.dtype, index, "q")
-    L = lib()
-    made = []
+    L, at = lib(), _place(index, stream)
     if out is None:
-        out = _like(q, rows, q_heads, dim)
+        out = _new(at, True, _like, q, rows, q_heads, dim)
         op, os_ = out.data_ptr(), q_heads * dim
-        made.append(out)
     else:
         op, os_, _, n = _heads(out, q_heads, dim, q.dtype, index, "out")
         if n != rows:
@@ -296,8 +312,7 @@ def kv8_attention(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, scale: floa
     lp = None
     if lse is not None and lse is not False:
         if lse is True:
-            lse = torch.empty((rows, q_heads), dtype=torch.float32, device=cache.device)
-            made.append(lse)
+            lse = _new(at, True, torch.empty, (rows, q_heads), dtype=torch.float32, device=cache.device)
         if tuple(_need(lse, torch.float32, 2, "lse").shape) != (rows, q_heads) or not lse.is_contiguous() or lse.get_device() != index:
             raise ValueError(f"lse must be a contiguous [{rows}][{q_heads}] on cuda:{index}")
         lp = lse.data_ptr()
@@ -305,8 +320,7 @@ def kv8_attention(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, scale: floa
     if workspace is None:
         wn = L.kv8_attention_workspace_bytes(cache._ref, batch._ref, q_heads, rows)
         if wn:
-            workspace = torch.empty(wn, dtype=torch.uint8, device=cache.device)
-            made.append(workspace)
+            workspace = _new(at, False, torch.empty, wn, dtype=torch.uint8, device=cache.device)
             wp = workspace.data_ptr()
     elif workspace.dtype != torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{index}")
@@ -314,7 +328,7 @@ def kv8_attention(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, scale: floa
         wp, wn = workspace.data_ptr(), workspace.numel()
     _call("kv8_attention", L.kv8_attention,
           (cache._ref, batch._ref, code, qp, qs, q_heads, rows, cache.scale if scale is None else scale, 1 if causal else 0, window,
-           op, os_, lp, wp, wn), index, stream, made)
+           op, os_, lp, wp, wn), index, at)
     return out if lp is None else (out, lse)
 
 
@@ -340,26 +354,24 @@ def kv8_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, inv_fr
         raise ValueError("q and k have different numbers of rows")
     pp, fp = _vector(pos, rows, torch.int32, index, "pos"), _vector(inv_freq, -1, torch.float32, index, "inv_freq")
     qw, kw = _vector(q_weight, dim, torch.float32, index, "q_weight"), _vector(k_weight, dim, torch.float32, index, "k_weight")
-    made = []
+    at = _place(index, stream)
     if q_out is None:
-        q_out = _like(q, rows, q_heads, dim)
+        q_out = _new(at, True, _like, q, rows, q_heads, dim)
         qop, qos = q_out.data_ptr(), q_heads * dim
-        made.append(q_out)
     else:
         qop, qos, _, n = _heads(q_out, q_heads, dim, dtype, index, "q_out")
         if n != rows:
             raise ValueError(f"q_out must have {rows} rows")
     if k_out is None:
-        k_out = _like(k, rows, k_heads, dim)
+        k_out = _new(at, True, _like, k, rows, k_heads, dim)
         kop, kos = k_out.data_ptr(), k_heads * dim
-        made.append(k_out)
     else:
         kop, kos, _, n = _heads(k_out, k_heads, dim, dtype, index, "k_out")
         if n != rows:
             raise ValueError(f"k_out must have {rows} rows")
     _call("kv8_qk_norm_rope", lib().kv8_qk_norm_rope,
           (code, rows, dim, qp, qs, q_heads, kp, ks, k_heads, pp, fp, 0 if fp is None else inv_freq.shape[0], 1 if neighbours else 0,
-           qw, kw, eps, qop, qos, kop, kos), index, stream, made)
+           qw, kw, eps, qop, qos, kop, kos), index, at)
     return q_out, k_out
 
 

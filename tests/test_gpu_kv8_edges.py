@@ -15,6 +15,7 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():
     pytest.skip("no GPU visible", allow_module_level=True)
 
+import test_gpu_kv8 as base  # noqa: E402
 from test_gpu_kv8 import F32, World, check_attention  # noqa: E402
 
 
@@ -50,3 +51,63 @@ def test_many_parts_join_the_first_rows_of_a_batch():
         w = World(5, 1, 64, 64, lens, news, lead=1)
         assert parts_of(w, 3, w.rows + 2) > 8
         check_attention(w, 3, F32, tag="many parts")
+
+
+# ---------------------------------------------------------------------------
+# Streams: what a call allocates
+
+def split_world(seed):
+    w = World(seed, 2, 128, 64, [3000, 900], [1, 1])
+    assert parts_of(w, 12, 2) > 1
+    return w, base.dev(w.values(2, F32, heads=12))
+
+
+def test_allocations_are_of_the_calls_stream(monkeypatch):
+    """A block of the current stream's memory may still be in use by work that
+    is queued there: another stream must not be given it."""
+    w, q = split_world(1)
+    k = base.dev(w.values(2, F32))
+    pos, freq = torch.arange(2, dtype=torch.int32, device=base.DEV), torch.ones(64, device=base.DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    made = []
+    for name in ("empty", "empty_like"):
+        def new(*args, fn=getattr(torch, name), **kw):
+            made.append(torch.cuda.current_stream().cuda_stream)
+            return fn(*args, **kw)
+        monkeypatch.setattr(torch, name, new)
+
+    def calls(stream):
+        del made[:]
+        out = kv8.kv8_attention(w.cache, w.batch, q, lse=True, stream=stream)
+        assert len(made) == 3  # out, lse, workspace
+        out += kv8.kv8_read(w.cache, w.batch, 2, stream=stream) + kv8.kv8_qk_norm_rope(q, k, pos, freq, stream=stream)
+        assert len(made) == 7
+        torch.cuda.synchronize()
+        return out
+
+    here = torch.cuda.current_stream().cuda_stream
+    want = calls(None)
+    assert set(made) == {here}
+    for stream in (side, side.cuda_stream):
+        got = calls(stream)
+        assert set(made) == {side.cuda_stream}
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with torch.cuda.stream(side):
+        got = calls(torch.cuda.default_stream().cuda_stream)  # 0
+        assert set(made) == {torch.cuda.default_stream().cuda_stream}
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_split_calls_on_two_streams_without_a_wait():
+    w, q = split_world(2)
+    x, p = split_world(3)
+    want = kv8.kv8_attention(w.cache, w.batch, q), kv8.kv8_attention(x.cache, x.batch, p)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(30):
+        got.append((kv8.kv8_attention(w.cache, w.batch, q), kv8.kv8_attention(x.cache, x.batch, p, stream=side)))
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
