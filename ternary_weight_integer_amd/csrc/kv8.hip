@@ -1687,6 +1687,21 @@ extern "C" size_t kv8_attention_workspace_bytes(const kv8_cache *cache, const kv
   return workspace_of(plan_of(c, s, batch->max_len, q_heads, 0, true), c, s, q_heads);
 }
 
+// What a kv8_attention call with these sizes runs: row_tiles of a wave of the
+// kernel for many rows (0: the kernel for few) and the parts that tokens are
+// cut into.  No part of the ABI: tests learn from it which kernel they test.
+extern "C" int kv8_attention_choice(const kv8_cache *cache, const kv8_batch *batch, int64_t q_heads, int64_t rows,
+                                    int causal, int64_t window, int *row_tiles, int *parts) {
+  Cache c;
+  Batch s;
+  if (const int st = check_attention(cache, batch, KV8_F32, q_heads, rows, c, s)) return st;
+  if (rows == 0 || s.seqs == 0 || window < 0) return I2S_EINVAL;
+  const Plan p = plan_of(c, s, batch->max_len, q_heads, window, causal != 0);
+  *row_tiles = p.row_tiles;
+  *parts = p.splits;
+  return I2S_OK;
+}
+
 extern "C" int kv8_attention(const kv8_cache *cache, const kv8_batch *batch, int type, const void *q, int64_t q_stride,
                              int64_t q_heads, int64_t rows, float scale, int causal, int64_t window, void *out,
                              int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes, void *stream) {

@@ -4,6 +4,8 @@ whose worlds are used."""
 
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -16,7 +18,7 @@ if not torch.cuda.is_available():
     pytest.skip("no GPU visible", allow_module_level=True)
 
 import test_gpu_kv8 as base  # noqa: E402
-from test_gpu_kv8 import F32, World, check_attention  # noqa: E402
+from test_gpu_kv8 import BF16, F16, F32, World, check_attention  # noqa: E402
 
 
 def parts_of(w, q_heads, rows):
@@ -111,3 +113,49 @@ def test_split_calls_on_two_streams_without_a_wait():
     torch.cuda.synchronize()
     for a, b in got:
         assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+
+
+# ---------------------------------------------------------------------------
+# Each form of the kernels
+
+def choice(w, q_heads, rows, causal=True, window=0):
+    """(row tiles of a wave, 0 where four waves share one; parts) of a call."""
+    row_tiles, parts = ctypes.c_int(), ctypes.c_int()
+    status = kv8.lib().kv8_attention_choice(ctypes.c_void_p(w.cache._ref), ctypes.c_void_p(w.batch._ref), ctypes.c_int64(q_heads),
+                                            ctypes.c_int64(rows), int(causal), ctypes.c_int64(window), ctypes.byref(row_tiles),
+                                            ctypes.byref(parts))
+    assert status == 0
+    return row_tiles.value, parts.value
+
+
+# (heads, D, P, group, lens, news, bound of the lengths, row tiles, split)
+LONG, SHORT = [330] + [70] * 12, [50] * 13
+FORMS = [
+    (2, 128, 64, 16, LONG, SHORT, 330, 1, False),
+    (2, 128, 64, 16, LONG, SHORT, 6000, 1, True),
+    (2, 128, 16, 16, LONG, SHORT, 330, 1, False),
+    (2, 128, 16, 16, LONG, SHORT, 6000, 1, True),
+    (1, 128, 256, 33, LONG, SHORT, 6000, 1, True),
+    (2, 96, 32, 20, LONG, SHORT, 6000, 1, True),
+    (1, 256, 64, 24, LONG, SHORT, 330, 1, False),
+    (1, 256, 16, 24, LONG, SHORT, 6000, 1, True),
+    (1, 160, 32, 28, LONG, SHORT, 330, 1, False),
+    (1, 208, 128, 28, LONG, SHORT, 6000, 1, True),
+    (2, 64, 64, 25, LONG, SHORT, 330, 1, False),
+    (2, 48, 16, 20, LONG, SHORT, 6000, 1, True),
+    (1, 16, 16, 5, [1200], [1000], 60000, 1, True),        # more parts than eight
+    (16, 64, 64, 4, [60, 40] * 30, [20, 37] * 30, 60, 2, False),
+    (16, 128, 128, 4, [130, 40] * 17, [20, 37] * 17, 130, 2, False),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("heads,D,P,group,lens,news,bound,row_tiles,split", FORMS)
+def test_every_form_of_the_kernel_for_many_rows(heads, D, P, group, lens, news, bound, row_tiles, split, dtype):
+    for causal, window, holes in ((True, 0, 0.0), (True, 150, 0.0), (False, 0, 0.1)):
+        w = World(D + P, heads, D, P, lens, news, holes=holes, lead=1, blocks=-(-max(lens) // P) + 2 if bound < 1000 else -(-bound // P))
+        w.batch = kv8.KV8Batch(w.batch.table, w.batch.lens, w.batch.starts, max_len=bound)
+        rows = w.rows + 2
+        chosen = choice(w, heads * group, rows, causal, window)
+        assert chosen[0] == row_tiles and (window or (chosen[1] > 1) == split), chosen
+        check_attention(w, group, dtype, causal=causal, window=window, tag=f"{chosen[0]} tiles, {chosen[1]} parts")
