@@ -554,13 +554,21 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Cache c, Batch s, T *__r
 // head's group, so that a group shares what is read of the cache) and walks
 // tiles of 64 tokens.  Everything stays in registers, operands are loaded
 // straight into the order of the matrix instructions:
-//   S^T = K Q^T   int8 16x16x64.  The codes are exact, a query is held as
-//     kDigits signed base-256 digits of its row's largest magnitude (3, 23
-//     bits, for F32 and F16 rows; 2, 15 bits, for BF16 rows, whose mantissas
-//     have 8), and the int32 dots are exact.
-//   O^T = V^T P^T  f16 16x16x32.  V's codes are exact in f16; a weight is one
-//     f16 (BF16 rows) or a sum of two (22 bits).  With one, and 2 digits, an
-//     F16 result's error was 1.3 times its own rounding.
+//   S^T = K Q^T   in one of two forms, in both of which a wide channel of a query
+//     takes nothing from its other components (with 23 bits of the row's largest
+//     magnitude F32 results were 60 times as far off as in F32 products where one
+//     component was 1000 times the rest, with 15 BF16 results twice their rounding):
+//     digits   int8 16x16x64.  The codes are exact, a query is four signed
+//       base-256 digits of a fixed-point number (its row's largest magnitude
+//       brought to 30 bits or more by a power of two), the int32 dots are exact.
+//     direct   f16 16x16x32, sums in F32.  The codes are exact.  An F16 query is
+//       its own operand, one of BF16 is exact when brought to 2^15 by a power of
+//       two (to 2^-40 of the row's largest magnitude), one of F32 is then the sum
+//       of two (22 bits).  The keys have to be turned into f16.
+//   O^T = V^T P^T  f16 16x16x32.  V's codes are exact in f16; a weight is the sum
+//     of two (22 bits), in BF16 rows one (11 bits: its rounding is an eighth of
+//     the result's own, and adds 0.6 to 0.8% to its error; a second costs a
+//     fifth of a prompt's time).
 // The rows of K's four 16-token operands are taken from the tile in the order
 // 16 (m / 4) + 4 j + m % 4, which leaves lane (row, g) with the logits of the
 // 16 consecutive tokens 16 g ..: those are its k indices of P^T, and one
@@ -601,16 +609,13 @@ struct Attend {
   int blocks, round;  // workgroups along the rows of one head and part, and those that fill the compute units once
 };
 
-// x less the kHalf-th of a pair of f16, exact where that is x rounded: one
-// mixed-precision operation (the compiler takes two).
-template <int kHalf>
-__device__ inline float less(float x, f16x2 pair) {
-  float r;
-  if (kHalf == 0) {
-    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[0,0,0] op_sel_hi:[1,0,0]" : "=v"(r) : "v"(pair), "v"(x));
-  } else {
-    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r) : "v"(pair), "v"(x));
-  }
+// What rounding x0 and x1 to the pair left, as a pair of its own: differences
+// that are exact, rounded once; one mixed-precision operation each (the compiler
+// takes three for two).
+__device__ inline f16x2 rest_of(float x0, float x1, f16x2 pair) {
+  f16x2 r;
+  asm("v_fma_mixlo_f16 %0, %1, -1.0, %2 op_sel:[0,0,0] op_sel_hi:[1,0,0]" : "=v"(r) : "v"(pair), "v"(x0));
+  asm("v_fma_mixhi_f16 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "+v"(r) : "v"(pair), "v"(x1));
   return r;
 }
 
@@ -761,10 +766,13 @@ struct Scales {
 // A wave's rows: queries, running statistics, results.  Lane (n, g) holds row
 // n of each row tile; of a tile of tokens its logits are those of the 16
 // tokens 16 g .., of a result the components 16 d + 4 g ...
-template <typename T, int kChunks, bool kFull, int kRowTiles>
+template <typename T, int kChunks, bool kFull, int kRowTiles, bool kDirect>
 struct Rows {
-  static constexpr int kDigits = std::is_same<T, bf16>::value ? 2 : 3;
-  static constexpr int kParts = kDigits - 1;             // f16 parts of a weight
+  static constexpr int kDigits = 4, kHalves = 2;
+  static constexpr int kTerms = std::is_same<T, float>::value ? 2 : 1;    // f16 terms of a query's component
+  static constexpr int kOperands = kDirect ? kHalves * kTerms : kDigits;  // of 64 components of the queries
+  static constexpr int kKeys = kDirect ? kHalves : 1;                     // of 64 components of 16 keys
+  static constexpr int kParts = std::is_same<T, bf16>::value ? 1 : 2;     // f16 parts of a weight
   static constexpr int kOut = 4 * kChunks;               // 16-component tiles
   typedef typename Row<T>::Vec Vec;
   static constexpr int kVecs = 16 / Row<T>::kValues;
@@ -776,7 +784,7 @@ struct Rows {
   const Attend &a;
   const int n, g, D;
   f32x4 acc[kRowTiles][kOut];
-  i32x4 q[kRowTiles][kChunks][kDigits];
+  i32x4 q[kRowTiles][kChunks][kOperands];
   float qs[kRowTiles], m[kRowTiles], l[kRowTiles];  // m: the running maximum less kHeadroom
   int lo[kRowTiles], hi[kRowTiles];
   int row_of[kRowTiles], head_of[kRowTiles];        // row_of: -1 behind the last row
@@ -804,7 +812,7 @@ struct Rows {
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
 #pragma unroll
-        for (int z = 0; z < kDigits; ++z) q[t][c][z] = i32x4{0, 0, 0, 0};
+        for (int z = 0; z < kOperands; ++z) q[t][c][z] = i32x4{0, 0, 0, 0};
       }
     }
   }
@@ -825,7 +833,7 @@ struct Rows {
     }
   }
 
-  // The loaded queries as digits.
+  // The loaded queries as operands.
   __device__ void set_queries() {
 #pragma unroll
     for (int t = 0; t < kRowTiles; ++t) {
@@ -842,48 +850,72 @@ struct Rows {
       }
       if (nan != 0.0f) amax = INFINITY;
       amax = over_lanes_max(amax);
-      constexpr float kTop = kDigits == 3 ? 127.0f * 65536.0f : 127.0f * 256.0f;
-      const float inv = amax > kMinScale && amax < INFINITY ? kTop / amax : 0.0f;
-      qs[t] = amax < INFINITY ? (amax > kMinScale ? amax / kTop * a.scale : 0.0f) : NAN;
+      // amax <= 127/128 2^over: the digits are at most 127, an f16 is below 2^15.
+      const int over = __builtin_amdgcn_frexp_expf(amax * 0.504f) + 1;
+      const int shift = !kDirect ? 8 * kDigits - 1 - over : std::is_same<T, f16>::value ? 0 : 15 - over;
+      qs[t] = amax < INFINITY ? ldexpf(a.scale, -shift) : NAN;
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
+        if constexpr (kDirect) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          // With 128 added to every digit the digits are the sum's bytes.
-          uint32_t u[4];
+          for (int z = 0; z < kHalves; ++z) {
+            f16x8 term[kTerms];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            u[k] = static_cast<uint32_t>(static_cast<int>(rintf(v[c][4 * w + k] * inv)) + (kDigits == 3 ? 0x808080 : 0x8080));
+            for (int k = 0; k < 8; ++k) {
+              const float x = ldexpf(v[c][8 * z + k], shift);
+              term[0][k] = static_cast<f16>(x);
+              if constexpr (kTerms == 2) term[1][k] = static_cast<f16>(x - static_cast<float>(term[0][k]));
+            }
 #pragma unroll
-          for (int z = 0; z < kDigits; ++z) {
-            const uint32_t byte = kDigits - 1 - z, pair = byte | (byte + 4) << 8 | 0x0c0c0000u;
-            const uint32_t low = __builtin_amdgcn_perm(u[1], u[0], pair), high = __builtin_amdgcn_perm(u[3], u[2], pair);
-            q[t][c][z][w] = static_cast<int>((low | high << 16) ^ 0x80808080u);
+            for (int i = 0; i < kTerms; ++i) q[t][c][z + kHalves * i] = __builtin_bit_cast(i32x4, term[i]);
+          }
+        } else {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            // With 128 added to every digit the digits are the sum's bytes.
+            uint32_t u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              u[k] = static_cast<uint32_t>(static_cast<int>(rintf(ldexpf(v[c][4 * w + k], shift)))) + 0x80808080u;
+#pragma unroll
+            for (int z = 0; z < kDigits; ++z) {
+              const uint32_t byte = kDigits - 1 - z, pair = byte | (byte + 4) << 8 | 0x0c0c0000u;
+              const uint32_t low = __builtin_amdgcn_perm(u[1], u[0], pair), high = __builtin_amdgcn_perm(u[3], u[2], pair);
+              q[t][c][z][w] = static_cast<int>((low | high << 16) ^ 0x80808080u);
+            }
           }
         }
       }
     }
   }
 
-  // Dots of row tile t with 16 tokens, K's operand given.
-  __device__ f32x4 dots(int t, const i32x4 (&k)[kChunks]) const {
-    i32x4 dot[kDigits];
+  // Dots of row tile t with 16 tokens, K's operands given.
+  __device__ f32x4 dots(int t, const i32x4 (&k)[kChunks][kKeys]) const {
+    if constexpr (kDirect) {
+      f32x4 f = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int z = 0; z < kDigits; ++z) {
-      dot[z] = i32x4{0, 0, 0, 0};
+      for (int c = 0; c < kChunks; ++c) {
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) dot[z] = __builtin_amdgcn_mfma_i32_16x16x64_i8(k[c], q[t][c][z], dot[z], 0, 0, 0);
-    }
-    f32x4 f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (kDigits == 3) {
-        f[i] = fmaf(static_cast<float>(dot[0][i]), 65536.0f, static_cast<float>(dot[1][i] * 256 + dot[kDigits - 1][i]));
-      } else {
-        f[i] = static_cast<float>(dot[0][i] * 256 + dot[1][i]);
+        for (int z = 0; z < kOperands; ++z)
+          f = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, k[c][z % kHalves]),
+                                                     __builtin_bit_cast(f16x8, q[t][c][z]), f, 0, 0, 0);
       }
+      return f;
+    } else {
+      i32x4 dot[kDigits];
+#pragma unroll
+      for (int z = 0; z < kDigits; ++z) {
+        dot[z] = i32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) dot[z] = __builtin_amdgcn_mfma_i32_16x16x64_i8(k[c][0], q[t][c][z], dot[z], 0, 0, 0);
+      }
+      // Two digits' dots are an int32 together: at most 2^8 x 256 x 2^14 + 2^22.
+      f32x4 f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        f[i] = fmaf(static_cast<float>(dot[0][i] * 256 + dot[1][i]), 65536.0f, static_cast<float>(dot[2][i] * 256 + dot[3][i]));
+      return f;
     }
-    return f;
   }
 
   // Weights of row tile t for the lane's tokens first .. first + 15, and the
@@ -928,10 +960,7 @@ struct Rows {
       sum += p0 + p1;
       const f16x2 near = {static_cast<f16>(p0), static_cast<f16>(p1)};
       w[0].pair[k / 2] = near;
-      if (kParts == 2) {
-        const f16x2 rest = {static_cast<f16>(less<0>(p0, near)), static_cast<f16>(less<1>(p1, near))};
-        w[kParts - 1].pair[k / 2] = rest;
-      }
+      if constexpr (kParts == 2) w[1].pair[k / 2] = rest_of(p0, p1, near);
     }
     l[t] = fmaf(sum, rvs, l[t]);
   }
@@ -995,7 +1024,7 @@ __device__ inline f16x8 codes_to_f16(int low, int high) {
 // kChunks: 64-component chunks of a head, kFull: the head fills them.
 template <typename T, int kChunks, bool kFull>
 __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_few_kernel(Attend a) {
-  typedef Rows<T, kChunks, kFull, 1> R;
+  typedef Rows<T, kChunks, kFull, 1, false> R;
   constexpr int kOut = R::kOut, kWaves = kThreads / 64, kStep = kWaves * kTile;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   Place w;
@@ -1010,7 +1039,7 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_few_k
   int t0 = part.begin + wave * kTile;
   if (t0 < part.end) {
     const Pages pages(a, w.p.b, w.h, D, part.end);
-    i32x4 kc[4][kChunks], vc[kOut];
+    i32x4 kc[4][kChunks][1], vc[kOut];
     Scales next;
     auto load_k = [&](int t, int entry) {
       const int8_t *q = pages.k + pages.page(entry) * pages.bytes + (pages.slot(t + kgroup) + (n & 3)) * D + 16 * g;
@@ -1018,7 +1047,7 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_few_k
       for (int j = 0; j < 4; ++j) {
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          if (kFull || 64 * c + 16 * g < D) kc[j][c] = *reinterpret_cast<const i32x4 *>(q + 4 * j * D + 64 * c);
+          if (kFull || 64 * c + 16 * g < D) kc[j][c][0] = *reinterpret_cast<const i32x4 *>(q + 4 * j * D + 64 * c);
         }
       }
     };
@@ -1031,7 +1060,7 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_few_k
     };
     if (!kFull) {
 #pragma unroll
-      for (int d = 0; d < kOut; ++d) vc[d] = kc[d & 3][d >> 2] = i32x4{0, 0, 0, 0};
+      for (int d = 0; d < kOut; ++d) vc[d] = kc[d & 3][d >> 2][0] = i32x4{0, 0, 0, 0};
     }
     rows.load_queries(w);
     int kpage = pages.entry(t0 + kgroup), vpage = pages.entry(t0 + 16 * g);
@@ -1104,21 +1133,25 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_few_k
 // Many rows (prompts, drafted tokens): each of the workgroup's 4 waves has
 // kRowTiles x 16 rows of its own, and all walk the same tiles.  A wave loads a
 // quarter of the next tile's operands while the present one is worked on,
-// turns its part of V into f16 (once for the workgroup), and lays both down
+// turns its part into f16 (once for the workgroup), and lays both down
 // in shared memory in the order in which lanes take them: 64 lanes x 16
 // bytes, free of bank conflicts.  Bound by issuing vector instructions (a
-// weight's exponent, sum and f16 parts, the digits' joining) and the matrix
+// weight's exponent, sum and f16 parts, the joining of digits) and the matrix
 // products, which a wave does by turns.  A causal prompt of 4096 F32 rows, 12
-// query heads over 2 of 128: 107 to 113 us, 0.47 PFLOP/s of the formula's
-// operations, 1.2 of those of three digits and two parts; vector instructions
-// are active in 55% of the SIMDs' cycles, the matrix units in 32%.  Six BF16
-// prompts of 150 to 5000 tokens, 16 query heads over 4 of 64, a window of 1024:
-// 145 us, 0.46 PFLOP/s; 78% and 18%.
+// query heads over 2 of 128: 118 us, 0.44 PFLOP/s of the formula's operations.
+// Six BF16 prompts of 150 to 5000 tokens, 16 query heads over 4 of 64, a window
+// of 1024: 136 us, 0.49 PFLOP/s.
 template <typename T, int kChunks, bool kFull, int kRowTiles>
 __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_many_kernel(Attend a) {
-  typedef Rows<T, kChunks, kFull, kRowTiles> R;
+  // F32 rows by digits where 48 KB of codes and V leave room for a third
+  // workgroup and f16 keys (64 KB) do not: one prompt of 4096 rows, 12 heads over
+  // 2 of 128, 118 against 120 us, chunks of 300 to 400 rows 85 against 87; with
+  // two row tiles (two workgroups in either form) directly: six prompts of 500 to
+  // 3000 rows, 16 heads over 4 of 128, 289 against 313 us.
+  constexpr bool kDirect = !(std::is_same<T, float>::value && kRowTiles == 1 && kChunks > 1);
+  typedef Rows<T, kChunks, kFull, kRowTiles, kDirect> R;
   constexpr int kOut = R::kOut, kRows = 16 * kRowTiles, kBlock = 4 * kRows;
-  __shared__ i32x4 lk[2][4][kChunks][64];
+  __shared__ i32x4 lk[2][4][kChunks][R::kKeys][64];
   __shared__ f16x8 lv[2][kOut][2][64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   Place w;
@@ -1158,7 +1191,13 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_many_
     auto lay_down = [&](int to) {
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
-        lk[to][wave][c][lane] = kc[c];
+        if constexpr (kDirect) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            lk[to][wave][c][k][lane] = __builtin_bit_cast(i32x4, codes_to_f16(kc[c][2 * k], kc[c][2 * k + 1]));
+        } else {
+          lk[to][wave][c][0][lane] = kc[c];
+        }
 #pragma unroll
         for (int k = 0; k < 2; ++k) lv[to][4 * c + wave][k][lane] = codes_to_f16(vc[c][2 * k], vc[c][2 * k + 1]);
       }
@@ -1215,16 +1254,16 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_many_
       typename R::Weights weights[kRowTiles][R::kParts];
       const bool edge = t0 < own.lo || t0 + kTile > own.hi || __any(now.hole);
       f32x4 f[kRowTiles][4];
-      i32x4 k[4][kChunks];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        i32x4 k[kChunks][R::kKeys];
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) k[j][c] = lk[from][j][c][lane];
-      }
+        for (int c = 0; c < kChunks; ++c) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+          for (int z = 0; z < R::kKeys; ++z) k[c][z] = lk[from][j][c][z][lane];
+        }
 #pragma unroll
-        for (int t = 0; t < kRowTiles; ++t) f[t][j] = rows.dots(t, k[j]);
+        for (int t = 0; t < kRowTiles; ++t) f[t][j] = rows.dots(t, k);
       }
 #pragma unroll
       for (int t = 0; t < kRowTiles; ++t) rows.weigh(t, f[t], now, t0 + 16 * g, edge, weights[t]);

@@ -159,3 +159,82 @@ def test_every_form_of_the_kernel_for_many_rows(heads, D, P, group, lens, news, 
         chosen = choice(w, heads * group, rows, causal, window)
         assert chosen[0] == row_tiles and (window or (chosen[1] > 1) == split), chosen
         check_attention(w, group, dtype, causal=causal, window=window, tag=f"{chosen[0]} tiles, {chosen[1]} parts")
+
+
+# ---------------------------------------------------------------------------
+# As exact as the plain form
+
+def plain_attention(w, q, scale):
+    """Causal attention in F32 products, exponents and sums."""
+    ref, out = w.ref, np.zeros(q.shape, np.float32)
+    group = q.shape[1] // ref.heads
+    for b, n in enumerate(ref.lens):
+        lo, hi = ref.starts[b], ref.starts[b + 1]
+        at, pos = ref.table[b, :-(-n // ref.P)], n - (hi - lo) + np.arange(hi - lo)
+        for h in range(ref.heads):
+            k = (ref.k[at, h].astype(np.float32) * ref.ks[at, h][:, None, None]).reshape(-1, ref.D)[:n]
+            v = (ref.v[at, h].astype(np.float32) * ref.vs[at, h][:, None, None]).swapaxes(1, 2).reshape(-1, ref.D)[:n]
+            for hq in range(h * group, (h + 1) * group):
+                e = np.float32(scale) * (q[lo:hi, hq] @ k.T)
+                e[np.arange(n)[None, :] > pos[:, None]] = -np.inf
+                p = np.exp(e - e.max(1, keepdims=True))
+                out[lo:hi, hq] = (p @ v) / p.sum(1, keepdims=True)
+    return out
+
+
+# (heads, D, P, group, lens, news, row tiles)
+EXACT = [
+    (2, 128, 64, 6, [2048], [1], 0),
+    (2, 64, 16, 3, [700, 300], [3, 40], 0),
+    (2, 128, 64, 16, LONG, SHORT, 1),
+    (16, 64, 64, 4, [60, 40] * 30, [20, 37] * 30, 2),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("heads,D,P,group,lens,news,row_tiles", EXACT)
+def test_wide_query_channels(heads, D, P, group, lens, news, row_tiles, dtype):
+    """One component of a query `wide` times the others, as the biases of
+    projections leave them, where keys are small: what is kept of the others
+    may not rest on it.  Root mean square errors against 64 bits: in 16-bit rows
+    the result's own rounding (2^-11, 2^-8 at most), besides which F32 sums and
+    22-bit weights (F16) are nothing and 11-bit weights (BF16) are 2^-11 to its
+    2^-8, 1 + 2^-7 times the whole; in F32 rows no more than three times the
+    plain form's, whose products and sums have 24 bits: a query's 22 bits (2^-23
+    on average at most, in each component) are twice its 2^-24, its sums and
+    exponents add as much as the plain form's own."""
+    for wide in (1.0, 30.0, 1000.0):
+        w = World(D + P, heads, D, P, lens, news)
+        q = w.rng.normal(0, 1, size=(w.rows, heads * group, D))
+        q[:, :, 5] *= wide
+        q = base.rounded(q, dtype)
+        w.ref.k[:, :, :, 5] = w.rng.integers(-1, 2, size=w.ref.k.shape[:3])
+        w.ref.ks[np.isfinite(w.ref.ks)] /= 4  # logits of a few units
+        w.cache = kv8.KV8Cache(base.dev(w.ref.k), base.dev(w.ref.v), base.dev(w.ref.ks), base.dev(w.ref.vs))
+        assert choice(w, heads * group, w.rows)[0] == row_tiles
+        scale = float(np.float32(D ** -0.5))
+        base.say(f"kv8 wide channel {wide} D={D} tiles={row_tiles} {dtype}")
+        exact = w.ref.attention(q, scale)["out"]
+        got = base.host(kv8.kv8_attention(w.cache, w.batch, base.dev(q, dtype), scale=scale))
+        rms = lambda a: float(np.sqrt(np.mean(np.square(a - exact))))  # noqa: E731
+        if dtype == F32:
+            own, allowed = rms(plain_attention(w, q, scale)), 3.0
+        else:
+            own, allowed = rms(base.rounded(exact, dtype)), 1.0 + 2.0 ** -7
+        base.say(f"  error {rms(got):.3g}, {rms(got) / own:.3f} of {own:.3g}")
+        assert rms(got) <= allowed * own
+
+
+@pytest.mark.parametrize("heads,D,P,group,lens,news,row_tiles", EXACT)
+def test_f16_rows_are_held_to_f32_weights(heads, D, P, group, lens, news, row_tiles):
+    """F16 queries are held exactly and weights in 22 bits: the bound that
+    test_gpu_kv8 derives for F32 rows, and half a step of the result."""
+    w = World(3 * D + P, heads, D, P, lens, news)
+    q = w.values(w.rows, F16, heads=heads * group, spread=0.4)
+    scale = float(np.float32(D ** -0.5))
+    assert choice(w, heads * group, w.rows)[0] == row_tiles
+    ref = w.ref.attention(q, scale)
+    out, lse = kv8.kv8_attention(w.cache, w.batch, base.dev(q, F16), scale=scale, lse=True)
+    tol, tol_lse = base.attention_bound(ref, w, F32, max(lens))
+    tol = tol + torch.finfo(F16).eps / 2 * np.abs(ref["out"]) + 2.0 ** -25
+    assert (np.abs(base.host(out) - ref["out"]) <= tol).all() and (np.abs(base.host(lse) - ref["lse"]) <= tol_lse).all()
