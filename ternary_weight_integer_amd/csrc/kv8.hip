@@ -578,7 +578,11 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Cache c, Batch s, T *__r
 //
 // The value scale is part of the weight: e = logit + log2(v_scale), running
 // maximum M over e, weight exp2(e - M + 15) (f16 then resolves weights down to
-// 2^-39 of the largest), and the denominator sums weight / v_scale.
+// 2^-39 of the largest), and the denominator sums weight / v_scale.  A scale
+// below kMinScale (0, say) counts as kMinScale there, so that the sum's terms,
+// 2^15 / 1e-20, stay in range, and as 0 in the result: what such pages leave in
+// it, at most kNothing, is far under the last bit of what an append's smallest
+// scale, 7.9e-8, makes, and is taken as 0.
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
@@ -586,7 +590,8 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kNoMax = -1e30f;   // running maximum of a row that has seen nothing
 constexpr float kHeadroom = 15.0f; // weights are at most 2^15
-constexpr float kMinScale = 1e-30f;
+constexpr float kMinScale = 1e-20f;
+constexpr float kNothing = 127.5f * kMinScale;
 constexpr int kTile = 64;          // tokens
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kMaxSplits = 256;
@@ -668,6 +673,16 @@ __device__ inline f16x4 codes_to_f16(int codes) {
   r.w[0] = __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u);
   r.w[1] = __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u);
   return r.h - static_cast<f16>(1152.0f);
+}
+
+// Four components of a result: o / l, with inv = 1 / l.
+__device__ inline f32x4 result_of(f32x4 o, float inv) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[i] *= inv;
+    o[i] = fabsf(o[i]) <= kNothing ? 0.0f : o[i];
+  }
+  return o;
 }
 
 template <typename T>
@@ -994,7 +1009,7 @@ struct Rows {
 #pragma unroll
       for (int i = 0; i < kCount; ++i) {
         const int d = first + i * stride;
-        if (kFull || 16 * d < D) store4(to + 16 * d, value(i) * inv);
+        if (kFull || 16 * d < D) store4(to + 16 * d, result_of(value(i), inv));
       }
       if (stats && a.lse) a.lse[at] = l[t] == 0.0f ? -INFINITY : kLn2 * (m[t] + log2f(l[t]));
     }
@@ -1342,7 +1357,7 @@ __global__ void __launch_bounds__(kThreads) join_few_kernel(Attend a, int block_
 #pragma unroll
     for (int k = 0; k < kFewParts; ++k)
       if (k < used) o += v[k][0] * *reinterpret_cast<const f32x4 *>(acc + k * static_cast<int64_t>(each) * D + 4 * c);
-    store4(out + 4 * c, o * inv);
+    store4(out + 4 * c, result_of(o, inv));
   }
   if (a.lse && lane == 0) a.lse[item] = l == 0.0f ? -INFINITY : kLn2 * (now + log2f(l));
 }
@@ -1385,7 +1400,7 @@ __global__ void __launch_bounds__(kThreads) join_many_kernel(Attend a, int block
 #pragma unroll
     for (int k = 1; k < 8; ++k) o += sums[k][tid];
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    store4(static_cast<T *>(a.out) + row * a.out_stride + static_cast<int64_t>(hq) * D + 4 * tid, o * inv);
+    store4(static_cast<T *>(a.out) + row * a.out_stride + static_cast<int64_t>(hq) * D + 4 * tid, result_of(o, inv));
   }
   if (a.lse && tid == 0) a.lse[at] = l == 0.0f ? -INFINITY : kLn2 * (now + log2f(l));
 }

@@ -238,3 +238,53 @@ def test_f16_rows_are_held_to_f32_weights(heads, D, P, group, lens, news, row_ti
     tol, tol_lse = base.attention_bound(ref, w, F32, max(lens))
     tol = tol + torch.finfo(F16).eps / 2 * np.abs(ref["out"]) + 2.0 ** -25
     assert (np.abs(base.host(out) - ref["out"]) <= tol).all() and (np.abs(base.host(lse) - ref["lse"]) <= tol_lse).all()
+
+
+# ---------------------------------------------------------------------------
+# Scales of zero
+
+def zero_bound(ref, w, n):
+    """That of test_gpu_kv8 for F32 rows, with exponents that hold a value
+    scale's logarithm of up to 67 (a scale of zero counts as 1e-20 in them)."""
+    out, lse = base.attention_bound(ref, w, F32, n)
+    more = 8 * base.U * 42
+    return out + 2 * more * ref["mag"], lse + more
+
+
+@pytest.mark.parametrize("heads,D,P,group,lens,news,bound", [
+    (1, 64, 64, 4, [20000, 300], [1, 1], 20000),       # few rows, split
+    (1, 64, 64, 4, [700], [1], 700),
+    (2, 128, 64, 16, LONG, SHORT, 330),                # many rows, one row tile
+    (2, 64, 32, 25, LONG, SHORT, 330),
+    (16, 64, 64, 4, [60, 40] * 30, [20, 37] * 30, 60),  # two
+])
+def test_value_scales_of_zero(heads, D, P, group, lens, news, bound):
+    """Pages of zeros (whatever their codes) add to the denominator alone."""
+    for which, by in (("all", 0.0), ("some", 0.0), ("some", 0.9e-20)):
+        w = World(D, heads, D, P, lens, news)
+        named = np.unique(w.ref.table[(w.ref.table >= 0) & (w.ref.table < w.ref.pages)])
+        hit = named if which == "all" else named[::2]
+        w.ref.vs[hit] = by
+        w.cache.v_scale.copy_(base.dev(w.ref.vs))
+        w.ref.vs[hit] = 0.0
+        q = w.values(w.rows, F32, heads=heads * group, spread=0.4)
+        scale = float(np.float32(D ** -0.5))
+        base.say(f"kv8 value scales of {by}: {which} D={D} lens={lens[:3]}")
+        ref = w.ref.attention(q, scale)
+        out, lse = (base.host(t) for t in kv8.kv8_attention(w.cache, w.batch, base.dev(q), scale=scale, lse=True))
+        if which == "all":
+            assert not out.any()
+        tol, tol_lse = zero_bound(ref, w, max(lens))
+        assert (np.abs(out - ref["out"]) <= tol).all() and (np.abs(lse - ref["lse"]) <= tol_lse).all()
+
+
+def test_a_new_cache_reads_as_zeros():
+    """Equal weights: a lane adds 16 of each of at most 100 tiles (116 u), log2
+    of the sum and the maximum less headroom are below 100 (a few u of that)."""
+    cache = kv8.new_cache(400, 1, 64, 64, device=base.DEV)
+    batch = kv8.KV8Batch(torch.arange(400, dtype=torch.int32, device=base.DEV)[None, :],
+                         torch.tensor([25600], dtype=torch.int32, device=base.DEV))
+    q = torch.ones((1, 3, 64), device=base.DEV)
+    out, lse = kv8.kv8_attention(cache, batch, q, lse=True)
+    assert not out.any()
+    assert (lse - np.log(25600)).abs().max() <= 1e-4
