@@ -131,6 +131,8 @@ size_t kv8_attention_workspace_bytes(const kv8_cache *cache, const kv8_batch *ba
  *   e_t = scale * sum_d q[d] * (k_scale * K_t[d])
  *   out = sum_t exp(e_t) * (v_scale * V_t) / sum_t exp(e_t)
  *   lse = log sum_t exp(e_t).
+ * Exponents e_t are F32: they resolve to their last bit, and have to stay in
+ * its range.
  * Value scales below 1e-20 count as 0 (their tokens still do in the sum).
  * A row that sees no token gives zeros and lse = -inf.  A query with a NaN or
  * an infinity gives NaN in its own output row and nowhere else.

@@ -588,8 +588,9 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
-constexpr float kNoMax = -1e30f;   // running maximum of a row that has seen nothing
+constexpr float kNoMax = -FLT_MAX; // running maximum of a row that has seen nothing
 constexpr float kHeadroom = 15.0f; // weights are at most 2^15
+constexpr float kSteady = 0x1p22f;  // of exponents: above, a product's rounding is 1/2 and more
 constexpr float kMinScale = 1e-20f;
 constexpr float kNothing = 127.5f * kMinScale;
 constexpr int kTile = 64;          // tokens
@@ -967,6 +968,18 @@ struct Rows {
       for (int d = 0; d < kOut; ++d) acc[t][d] *= shrink;
 #pragma unroll
       for (int k = 0; k < 16; ++k) e[k] = e[k] == -INFINITY ? e[k] : fmaf(f[k / 4][k % 4], ck, lvs - now);
+      // A maximum whose last bit is 1/2 or more misses the exponents that made it
+      // by as much: the largest is set to weigh 2^15 all the same.
+      const bool large = fabsf(now) > kSteady && now != kNoMax;
+      if (__any(large)) {
+        float most = e[0];
+#pragma unroll
+        for (int k = 1; k < 16; ++k) most = fmaxf(most, e[k]);
+        most = over_lanes_max(most) - kHeadroom;
+        most = large && (most > 0.0f || now == top) ? most : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) e[k] -= most;
+      }
     }
     float sum = 0.0f;
 #pragma unroll
@@ -1156,14 +1169,21 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_few_k
 // query heads over 2 of 128: 118 us, 0.44 PFLOP/s of the formula's operations.
 // Six BF16 prompts of 150 to 5000 tokens, 16 query heads over 4 of 64, a window
 // of 1024: 136 us, 0.49 PFLOP/s.
+//
+// F32 rows by digits where 48 KB of codes and V leave room for a third
+// workgroup and f16 keys (64 KB) do not: one prompt of 4096 rows, 12 heads over
+// 2 of 128, 118 against 120 us, chunks of 300 to 400 rows 85 against 87; with
+// two row tiles (two workgroups in either form) directly: six prompts of 500 to
+// 3000 rows, 16 heads over 4 of 128, 289 against 313 us.
+template <typename T, int kChunks, int kRowTiles>
+struct Many {
+  static constexpr bool kDirect = !(std::is_same<T, float>::value && kRowTiles == 1 && kChunks > 1);
+  static constexpr int kGroups = kChunks > 2 ? 1 : kDirect ? 2 : 3;  // workgroups on a unit, at least
+};
+
 template <typename T, int kChunks, bool kFull, int kRowTiles>
-__global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_many_kernel(Attend a) {
-  // F32 rows by digits where 48 KB of codes and V leave room for a third
-  // workgroup and f16 keys (64 KB) do not: one prompt of 4096 rows, 12 heads over
-  // 2 of 128, 118 against 120 us, chunks of 300 to 400 rows 85 against 87; with
-  // two row tiles (two workgroups in either form) directly: six prompts of 500 to
-  // 3000 rows, 16 heads over 4 of 128, 289 against 313 us.
-  constexpr bool kDirect = !(std::is_same<T, float>::value && kRowTiles == 1 && kChunks > 1);
+__global__ void __launch_bounds__(kThreads, (Many<T, kChunks, kRowTiles>::kGroups)) attention_many_kernel(Attend a) {
+  constexpr bool kDirect = Many<T, kChunks, kRowTiles>::kDirect;
   typedef Rows<T, kChunks, kFull, kRowTiles, kDirect> R;
   constexpr int kOut = R::kOut, kRows = 16 * kRowTiles, kBlock = 4 * kRows;
   __shared__ i32x4 lk[2][4][kChunks][R::kKeys][64];

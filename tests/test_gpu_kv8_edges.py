@@ -288,3 +288,41 @@ def test_a_new_cache_reads_as_zeros():
     out, lse = kv8.kv8_attention(cache, batch, q, lse=True)
     assert not out.any()
     assert (lse - np.log(25600)).abs().max() <= 1e-4
+
+
+# ---------------------------------------------------------------------------
+# Large exponents
+
+@pytest.mark.parametrize("dtype,sizes", [(F32, (1e4, 1e6, 1e7, 1e9, 3e20, 1e30, 3e34)), (F16, (400,)), (BF16, (1e9, 3e34))])
+@pytest.mark.parametrize("heads,D,P,group,lens,news,row_tiles", EXACT)
+def test_large_exponents(heads, D, P, group, lens, news, row_tiles, dtype, sizes):
+    """Exponents that rise with the token by 2^-6 |q| scale, at least 100, to as
+    much as 1e36, of either sign: the largest (a row's last token, or the first)
+    takes all.  Its weight is rounded like its share of the sum, then the
+    reciprocals, the product and the result: 16 u, and half a step of the type.
+    Where all keys are equal, means of the values, whatever the weights."""
+    scale = 1e5 if dtype == F16 else 1.0
+    for size in sizes:
+        for equal in (False, True):
+            w = World(D + P, heads, D, P, lens, news)
+            w.ref.ks[:], w.ref.vs[:] = 2.0 ** -6, np.nan_to_num(w.ref.vs, nan=0.1)
+            w.ref.k[:, :, :, :2] = 50
+            for b, n in enumerate(lens):
+                for t in range(0 if equal else n):  # 128 (t / 100) + t % 100 in all
+                    w.ref.k[w.ref.table[b, t // P], :, t % P, :2] = t // 100, t % 100
+            w.cache = kv8.KV8Cache(*(base.dev(a) for a in (w.ref.k, w.ref.v, w.ref.ks, w.ref.vs)))
+            q = np.zeros((w.rows, heads * group, D))
+            q[:, :, 1] = size * w.rng.choice([-1.0, 1.0], size=q.shape[:2])
+            q = base.rounded(q, dtype)
+            q[:, :, 0] = 128 * q[:, :, 1]
+            assert choice(w, heads * group, w.rows)[0] == row_tiles
+            base.say(f"kv8 large exponents {size} equal={equal} D={D} tiles={row_tiles} {dtype}")
+            out, lse = (base.host(t) for t in kv8.kv8_attention(w.cache, w.batch, base.dev(q, dtype), scale=scale, lse=True))
+            ref = w.ref.attention(q, scale)
+            assert np.isfinite(out).all()
+            assert (np.abs(lse - ref["lse"]) <= 8 * base.U * np.abs(ref["lse"]) + 1e-3).all()
+            if equal:
+                assert (np.abs(out) <= 127.5 * w.ref.vs.max()).all()
+            else:
+                tol = 16 * base.U * ref["mag"] + torch.finfo(dtype).eps / 2 * np.abs(ref["out"]) + 2.0 ** -25
+                assert (np.abs(out - ref["out"]) <= tol).all()
