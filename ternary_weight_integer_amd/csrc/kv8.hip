@@ -1637,6 +1637,9 @@ Plan plan_for(int row_tiles, const Cache &c, const Batch &s, int64_t len, int64_
   return p;
 }
 
+// Positions are below kMaxRows: a window of that many tokens or more is none.
+inline int64_t window_of(int64_t window) { return window < kMaxRows ? window : 0; }
+
 // The workspace is sized without a window, which only takes parts away.
 Plan plan_of(const Cache &c, const Batch &s, int64_t max_len, int64_t q_heads, int64_t window, bool causal) {
   const int64_t group = q_heads / c.heads, rows = s.rows * group / s.seqs;  // of a sequence, on average
@@ -1770,7 +1773,7 @@ extern "C" int kv8_attention_choice(const kv8_cache *cache, const kv8_batch *bat
   Batch s;
   if (const int st = check_attention(cache, batch, KV8_F32, q_heads, rows, c, s)) return st;
   if (rows == 0 || s.seqs == 0 || window < 0) return I2S_EINVAL;
-  const Plan p = plan_of(c, s, batch->max_len, q_heads, window, causal != 0);
+  const Plan p = plan_of(c, s, batch->max_len, q_heads, window_of(window), causal != 0);
   *row_tiles = p.row_tiles;
   *parts = p.splits;
   return I2S_OK;
@@ -1787,7 +1790,7 @@ extern "C" int kv8_attention(const kv8_cache *cache, const kv8_batch *batch, int
   if (bad_rows(q, q_stride, width, value_bytes(type)) || bad_rows(out, out_stride, width, value_bytes(type)) ||
       !aligned(lse, 4))
     return I2S_EINVAL;
-  const Plan p = plan_of(a.c, a.s, batch->max_len, q_heads, window, causal != 0);
+  const Plan p = plan_of(a.c, a.s, batch->max_len, q_heads, window_of(window), causal != 0);
   if (p.blocks * a.c.heads * p.splits > 0x7fffffff || rows * q_heads > 0x7fffffff) return I2S_ERANGE;
   const size_t need = workspace_of(p, a.c, a.s, q_heads);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return I2S_EWORKSPACE;
@@ -1798,7 +1801,7 @@ extern "C" int kv8_attention(const kv8_cache *cache, const kv8_batch *batch, int
   a.ml = need ? a.acc + static_cast<int64_t>(p.splits) * rows * q_heads * a.c.dim : nullptr;
   a.q_stride = q_stride;
   a.out_stride = out_stride;
-  a.window = window < kMaxRows ? static_cast<int>(window) : 0;  // positions are below kMaxRows
+  a.window = static_cast<int>(window_of(window));
   a.scale = scale * 1.44269504088896341f;
   a.q_heads = static_cast<int>(q_heads);
   a.group = static_cast<int>(q_heads / a.c.heads);
