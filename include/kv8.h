@@ -43,9 +43,10 @@
  * caller, on the device that is current; `stream` is a hipStream_t or NULL;
  * arguments are checked on the host before anything is launched, calls
  * neither allocate nor synchronize, and keep nothing from one call to the
- * next.  Structs are host memory, read before the call returns.  Lengths,
- * starts, positions and the table are read on the device when the kernels
- * run, so a captured graph follows their contents.
+ * next.  Structs are host memory, read before the call returns.  Strides are
+ * at most 2^40 elements (I2S_ERANGE beyond).  Lengths, starts, positions and
+ * the table are read on the device when the kernels run, so a captured graph
+ * follows their contents.
  */
 #ifndef KV8_H
 #define KV8_H

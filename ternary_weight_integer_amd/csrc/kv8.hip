@@ -1526,8 +1526,12 @@ inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintp
 
 inline int value_bytes(int type) { return type == KV8_F32 ? 4 : type == KV8_F16 || type == KV8_BF16 ? 2 : 0; }
 
-inline bool bad_rows(const void *p, int64_t stride, int64_t width, int size) {
-  return !p || !aligned(p, 16) || stride < width || (stride * size) % 16 != 0;
+constexpr int64_t kMaxStride = INT64_C(1) << 40;
+
+// I2S_OK, or what is wrong with rows of `width` values of `size` bytes.
+inline int check_rows(const void *p, int64_t stride, int64_t width, int size) {
+  if (!p || !aligned(p, 16) || stride < width || stride % (16 / size) != 0) return I2S_EINVAL;
+  return stride > kMaxStride ? I2S_ERANGE : I2S_OK;
 }
 
 int check_batch(const kv8_cache *c, const kv8_batch *b, int type, int64_t rows, Cache &dc, Batch &db) {
@@ -1540,7 +1544,7 @@ int check_batch(const kv8_cache *c, const kv8_batch *b, int type, int64_t rows, 
     return I2S_EALIGN;
   if (b->seqs < 0 || b->blocks < 0 || b->table_stride < b->blocks || b->max_len < 0) return I2S_EINVAL;
   if (c->pages > 0x7fffffff || c->heads > 1024 || b->seqs > kMaxSeqs || b->blocks > 0x7fffffff || rows > kMaxRows ||
-      b->table_stride > (INT64_C(1) << 40))
+      b->table_stride > kMaxStride)
     return I2S_ERANGE;
   if (b->seqs > 0 && (!b->lens || !aligned(b->lens, 4) || (b->blocks > 0 && !b->table) || !aligned(b->table, 4) ||
                       !aligned(b->starts, 4)))
@@ -1713,7 +1717,8 @@ extern "C" int kv8_append(const kv8_cache *cache, const kv8_batch *batch, int ty
   if (const int st = check_batch(cache, batch, type, rows, c, s)) return st;
   if (rows == 0 || s.seqs == 0) return I2S_OK;
   const int64_t width = static_cast<int64_t>(c.heads) * c.dim;
-  if (bad_rows(k, k_stride, width, value_bytes(type)) || bad_rows(v, v_stride, width, value_bytes(type))) return I2S_EINVAL;
+  if (const int st = check_rows(k, k_stride, width, value_bytes(type))) return st;
+  if (const int st = check_rows(v, v_stride, width, value_bytes(type))) return st;
   const Items n(c, s, true);
   if (n.blocks > 0x7fffffff || n.items / 2 > 0x7fffffff) return I2S_ERANGE;
   return by_type(type, [&](auto t) {
@@ -1738,7 +1743,8 @@ extern "C" int kv8_read(const kv8_cache *cache, const kv8_batch *batch, int type
   if (const int st = check_batch(cache, batch, type, rows, c, s)) return st;
   if (rows == 0 || s.seqs == 0) return I2S_OK;
   const int64_t width = static_cast<int64_t>(c.heads) * c.dim;
-  if (bad_rows(k, k_stride, width, value_bytes(type)) || bad_rows(v, v_stride, width, value_bytes(type))) return I2S_EINVAL;
+  if (const int st = check_rows(k, k_stride, width, value_bytes(type))) return st;
+  if (const int st = check_rows(v, v_stride, width, value_bytes(type))) return st;
   const Items n(c, s, false);
   if (n.blocks > 0x7fffffff || n.items / 2 > 0x7fffffff) return I2S_ERANGE;
   return by_type(type, [&](auto t) {
@@ -1787,9 +1793,9 @@ extern "C" int kv8_attention(const kv8_cache *cache, const kv8_batch *batch, int
   if (window < 0 || !(fabsf(scale) < INFINITY)) return I2S_EINVAL;
   if (rows == 0 || a.s.seqs == 0) return I2S_OK;
   const int64_t width = q_heads * a.c.dim;
-  if (bad_rows(q, q_stride, width, value_bytes(type)) || bad_rows(out, out_stride, width, value_bytes(type)) ||
-      !aligned(lse, 4))
-    return I2S_EINVAL;
+  if (const int st = check_rows(q, q_stride, width, value_bytes(type))) return st;
+  if (const int st = check_rows(out, out_stride, width, value_bytes(type))) return st;
+  if (!aligned(lse, 4)) return I2S_EINVAL;
   const Plan p = plan_of(a.c, a.s, batch->max_len, q_heads, window_of(window), causal != 0);
   if (p.blocks * a.c.heads * p.splits > 0x7fffffff || rows * q_heads > 0x7fffffff) return I2S_ERANGE;
   const size_t need = workspace_of(p, a.c, a.s, q_heads);
@@ -1845,10 +1851,14 @@ extern "C" int kv8_qk_norm_rope(int type, int64_t rows, int64_t dim, const void 
   if (dim < 16 || dim > KV8_MAX_DIM || dim % 16 || pairs % 8 || 2 * pairs > dim) return I2S_EALIGN;
   if (rows > kMaxRows || q_heads > 65535 || k_heads > 65535) return I2S_ERANGE;
   if (rows == 0 || q_heads + k_heads == 0) return I2S_OK;
-  if (q_heads > 0 && (bad_rows(q, q_stride, q_heads * dim, size) || bad_rows(q_out, q_out_stride, q_heads * dim, size)))
-    return I2S_EINVAL;
-  if (k_heads > 0 && (bad_rows(k, k_stride, k_heads * dim, size) || bad_rows(k_out, k_out_stride, k_heads * dim, size)))
-    return I2S_EINVAL;
+  if (q_heads > 0) {
+    if (const int st = check_rows(q, q_stride, q_heads * dim, size)) return st;
+    if (const int st = check_rows(q_out, q_out_stride, q_heads * dim, size)) return st;
+  }
+  if (k_heads > 0) {
+    if (const int st = check_rows(k, k_stride, k_heads * dim, size)) return st;
+    if (const int st = check_rows(k_out, k_out_stride, k_heads * dim, size)) return st;
+  }
   if (!pos || !aligned(pos, 4) || (pairs > 0 && !inv_freq) || !aligned(inv_freq, 4) || !aligned(q_weight, 4) ||
       !aligned(k_weight, 4))
     return I2S_EINVAL;
