@@ -35,9 +35,9 @@
  * starts[b] + i is the token at position lens[b] - n_b + i.  With starts NULL
  * every sequence has rows / seqs rows.  The same batch serves the append, the
  * attention and a read-back of one step.  A row whose position is negative
- * (n_b > lens[b]) is dropped by the append, is read back as zeros, and
- * attends to nothing.  Rows outside starts[0] .. starts[seqs]-1 are left as
- * they were.
+ * (n_b > lens[b]) is dropped by the append and read back as zeros; a causal
+ * attention lets it see nothing, any other what its formula says.  Rows outside
+ * starts[0] .. starts[seqs]-1 are left as they were.
  *
  * Conventions as in i2s.h: data pointers are device pointers owned by the
  * caller, on the device that is current; `stream` is a hipStream_t or NULL;

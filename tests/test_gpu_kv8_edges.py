@@ -326,3 +326,23 @@ def test_large_exponents(heads, D, P, group, lens, news, row_tiles, dtype, sizes
             else:
                 tol = 16 * base.U * ref["mag"] + torch.finfo(dtype).eps / 2 * np.abs(ref["out"]) + 2.0 ** -25
                 assert (np.abs(out - ref["out"]) <= tol).all()
+
+
+# ---------------------------------------------------------------------------
+# Rows in front of position 0
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_in_front_of_position_0(dtype):
+    """They see nothing where causal.  Else they see as any row does: with the
+    query of a row at position 0 or later, and no window, the same."""
+    w = World(70, 2, 64, 16, [3, 40], [9, 4])  # positions -6 .. 2 and 36 .. 39
+    q = w.values(13, dtype, heads=6)
+    q[0] = q[5] = q[8]
+    for window in (0, 7):
+        check_attention(w, 3, dtype, causal=True, window=window, rows=13, q=q, tag="in front")
+        check_attention(w, 3, dtype, causal=False, window=window, rows=13, q=q, tag="in front")
+    out, lse = kv8.kv8_attention(w.cache, w.batch, base.dev(q, dtype), lse=True)
+    assert not out[:6].any() and torch.isneginf(lse[:6]).all()
+    out, lse = kv8.kv8_attention(w.cache, w.batch, base.dev(q, dtype), causal=False, lse=True)
+    for row in (0, 5):
+        assert torch.equal(out[row], out[8]) and torch.equal(lse[row], lse[8])
