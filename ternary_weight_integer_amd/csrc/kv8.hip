@@ -566,9 +566,10 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Cache c, Batch s, T *__r
 //       two (to 2^-40 of the row's largest magnitude), one of F32 is then the sum
 //       of two (22 bits).  The keys have to be turned into f16.
 //   O^T = V^T P^T  f16 16x16x32.  V's codes are exact in f16; a weight is the sum
-//     of two (22 bits), in BF16 rows one (11 bits: its rounding is an eighth of
-//     the result's own, and adds 0.6 to 0.8% to its error; a second costs a
-//     fifth of a prompt's time).
+//     of two (22 bits), where many BF16 rows are worked on one (11 bits: its
+//     rounding is an eighth of the result's own, and adds 0.5 to 0.8% to its
+//     error; a second takes 18 to 20% of a prompt's time, and 0.7% where few rows
+//     wait for the cache).
 // The rows of K's four 16-token operands are taken from the tile in the order
 // 16 (m / 4) + 4 j + m % 4, which leaves lane (row, g) with the logits of the
 // 16 consecutive tokens 16 g ..: those are its k indices of P^T, and one
@@ -782,13 +783,13 @@ struct Scales {
 // A wave's rows: queries, running statistics, results.  Lane (n, g) holds row
 // n of each row tile; of a tile of tokens its logits are those of the 16
 // tokens 16 g .., of a result the components 16 d + 4 g ...
-template <typename T, int kChunks, bool kFull, int kRowTiles, bool kDirect>
+template <typename T, int kChunks, bool kFull, int kRowTiles, bool kDirect, int kWeightParts>
 struct Rows {
   static constexpr int kDigits = 4, kHalves = 2;
   static constexpr int kTerms = std::is_same<T, float>::value ? 2 : 1;    // f16 terms of a query's component
   static constexpr int kOperands = kDirect ? kHalves * kTerms : kDigits;  // of 64 components of the queries
   static constexpr int kKeys = kDirect ? kHalves : 1;                     // of 64 components of 16 keys
-  static constexpr int kParts = std::is_same<T, bf16>::value ? 1 : 2;     // f16 parts of a weight
+  static constexpr int kParts = kWeightParts;                             // f16 parts of a weight
   static constexpr int kOut = 4 * kChunks;               // 16-component tiles
   typedef typename Row<T>::Vec Vec;
   static constexpr int kVecs = 16 / Row<T>::kValues;
@@ -1052,7 +1053,7 @@ __device__ inline f16x8 codes_to_f16(int low, int high) {
 // kChunks: 64-component chunks of a head, kFull: the head fills them.
 template <typename T, int kChunks, bool kFull>
 __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_few_kernel(Attend a) {
-  typedef Rows<T, kChunks, kFull, 1, false> R;
+  typedef Rows<T, kChunks, kFull, 1, false, 2> R;
   constexpr int kOut = R::kOut, kWaves = kThreads / 64, kStep = kWaves * kTile;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   Place w;
@@ -1184,7 +1185,7 @@ struct Many {
 template <typename T, int kChunks, bool kFull, int kRowTiles>
 __global__ void __launch_bounds__(kThreads, (Many<T, kChunks, kRowTiles>::kGroups)) attention_many_kernel(Attend a) {
   constexpr bool kDirect = Many<T, kChunks, kRowTiles>::kDirect;
-  typedef Rows<T, kChunks, kFull, kRowTiles, kDirect> R;
+  typedef Rows<T, kChunks, kFull, kRowTiles, kDirect, std::is_same<T, bf16>::value ? 1 : 2> R;
   constexpr int kOut = R::kOut, kRows = 16 * kRowTiles, kBlock = 4 * kRows;
   __shared__ i32x4 lk[2][4][kChunks][R::kKeys][64];
   __shared__ f16x8 lv[2][kOut][2][64];

@@ -346,3 +346,43 @@ def test_rows_in_front_of_position_0(dtype):
     out, lse = kv8.kv8_attention(w.cache, w.batch, base.dev(q, dtype), causal=False, lse=True)
     for row in (0, 5):
         assert torch.equal(out[row], out[8]) and torch.equal(lse[row], lse[8])
+
+
+@pytest.mark.parametrize("heads,D,P,group,lens,news", [(2, 128, 64, 6, [2048], [1]), (2, 64, 16, 3, [700, 300], [3, 12]),
+                                                       (1, 256, 64, 4, [900], [2])])
+def test_few_bf16_rows_are_held_to_the_bound_of_f32(heads, D, P, group, lens, news):
+    """Queries in 30 bits and weights in 22, whatever the rows' type: the bound
+    of F32 rows, and half a step of the result."""
+    w = World(5 * D + P, heads, D, P, lens, news)
+    q = w.values(w.rows, BF16, heads=heads * group, spread=0.4)
+    scale = float(np.float32(D ** -0.5))
+    assert choice(w, heads * group, w.rows)[0] == 0
+    ref = w.ref.attention(q, scale)
+    out, lse = kv8.kv8_attention(w.cache, w.batch, base.dev(q, BF16), scale=scale, lse=True)
+    tol, tol_lse = base.attention_bound(ref, w, F32, max(lens))
+    tol = tol + torch.finfo(BF16).eps / 2 * np.abs(ref["out"])
+    assert (np.abs(base.host(out) - ref["out"]) <= tol).all() and (np.abs(base.host(lse) - ref["lse"]) <= tol_lse).all()
+
+
+@pytest.mark.parametrize("D,P,lens,news", [(128, 64, [100], [1]), (64, 16, [90, 120], [1, 1]), (256, 64, [60], [1])])
+def test_few_bf16_rows_whose_values_cancel(D, P, lens, news):
+    """Tokens of two kinds in turn, values +100 and -100, exponents that differ
+    by less than 0.01: results are a hundredth of what they are made of, and half
+    a step of theirs is nothing beside a rounding of the weights to 11 bits, up
+    to 2^-13 of the values (the smaller kind's 2^-12, halved)."""
+    w = World(D, 2, D, P, lens, news)
+    w.ref.k[:, :, :, 0] = 100 - np.arange(P) % 2
+    w.ref.v[:] = np.where(np.arange(P) % 2, -100, 100)
+    w.ref.ks[:] = w.ref.vs[:] = 2.0 ** -6
+    w.cache = kv8.KV8Cache(*(base.dev(a) for a in (w.ref.k, w.ref.v, w.ref.ks, w.ref.vs)))
+    q = np.zeros((w.rows, 2 * 33, D))
+    q[:, :, 0] = w.rng.uniform(0.5, 2.0, size=q.shape[:2])
+    q = base.rounded(q, BF16)
+    assert choice(w, 66, w.rows)[0] == 0
+    ref = w.ref.attention(q, 0.2)
+    out = base.host(kv8.kv8_attention(w.cache, w.batch, base.dev(q, BF16), scale=0.2))
+    # As in test_gpu_kv8, but that a query's one component is held exactly.
+    n, weight = max(lens), 8 * base.U * (2 * ref["top"] + 25) + 4 * base.U
+    tol = ref["mag"] * (2 * weight + 2 * n * base.U + 2.0 ** -22)[..., None] + torch.finfo(BF16).eps / 2 * np.abs(ref["out"])
+    assert tol.max() < 2.0 ** -14 * ref["mag"].max()
+    assert (np.abs(out - ref["out"]) <= tol).all()
