@@ -178,13 +178,13 @@ class _Apart:
             else:
                 self.other = torch.cuda.default_stream(index)
 
-    def new(self, kept: bool, fn, *args, **kw) -> torch.Tensor:
-        """fn(*args, **kw), a new tensor: of the memory of the call's stream,
-        and recorded on the current one if the caller gets it (kept)."""
+    def new(self, kept: bool, shape, dtype, device) -> torch.Tensor:
+        """A new tensor of the memory of the call's stream, recorded on the
+        current one if the caller gets it (kept)."""
         if self.other is None:
-            return fn(*args, **kw)
+            return torch.empty(shape, dtype=dtype, device=device)
         with torch.cuda.stream(self.other):
-            t = fn(*args, **kw)
+            t = torch.empty(shape, dtype=dtype, device=device)
         if kept:
             t.record_stream(torch.cuda.current_stream(self.index))
         return t
@@ -197,10 +197,6 @@ class _Apart:
 def _place(index: int, stream):
     """Where a call runs: None for the current stream of the current device."""
     return None if stream is None and index == _current() else _Apart(index, stream)
-
-
-def _new(at, kept: bool, fn, *args, **kw) -> torch.Tensor:
-    return fn(*args, **kw) if at is None else at.new(kept, fn, *args, **kw)
 
 
 def _call(name: str, fn, args, index: int, at):
@@ -231,9 +227,14 @@ def _heads(t, heads, dim: int, dtype, index: int, name: str):
     return t.data_ptr(), (stride[0] if rows > 1 else h * d), h, rows
 
 
-def _like(t, rows: int, heads: int, dim: int) -> torch.Tensor:
+def _dense(at, shape, dtype, device, kept: bool = True) -> torch.Tensor:
+    """A new tensor for a call that runs at `at`."""
+    return torch.empty(shape, dtype=dtype, device=device) if at is None else at.new(kept, shape, dtype, device)
+
+
+def _like(t, rows: int, heads: int, dim: int, at) -> torch.Tensor:
     """A dense tensor of t's shape, type and device."""
-    return torch.empty_like(t) if t.is_contiguous() else torch.empty((rows, heads, dim), dtype=t.dtype, device=t.device)
+    return torch.empty_like(t) if at is None and t.is_contiguous() else _dense(at, (rows, heads, dim), t.dtype, t.device)
 
 
 def _type(t, name: str) -> int:
@@ -268,16 +269,16 @@ def kv8_read(cache: KV8Cache, batch: KV8Batch, rows: int, dtype=torch.float32, k
     heads, dim = cache.heads, cache.dim
     given = k if k is not None else v
     dtype = dtype if given is None else given.dtype
-    at = _place(index, stream)
+    at, made = _place(index, stream), False
     if k is None:
-        k = _new(at, True, torch.empty, (rows, heads, dim), dtype=dtype, device=cache.device)
-        kp, ks = k.data_ptr(), heads * dim
+        k = _dense(at, (rows, heads, dim), dtype, cache.device)
+        kp, ks, made = k.data_ptr(), heads * dim, True
     else:
         kp, ks, _, n = _heads(k, heads, dim, dtype, index, "k")
         if n != rows:
             raise ValueError(f"k must have {rows} rows")
     if v is None:
-        v = _new(at, True, torch.empty, (rows, heads, dim), dtype=dtype, device=cache.device)
+        v = torch.empty_like(k) if made and at is None else _dense(at, (rows, heads, dim), dtype, cache.device)
         vp, vs = v.data_ptr(), heads * dim
     else:
         vp, vs, _, n = _heads(v, heads, dim, dtype, index, "v")
@@ -303,7 +304,7 @@ def kv8_attention(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, scale: floa
     qp, qs, q_heads, rows = _heads(q, None, dim, q.dtype, index, "q")
     L, at = lib(), _place(index, stream)
     if out is None:
-        out = _new(at, True, _like, q, rows, q_heads, dim)
+        out = _like(q, rows, q_heads, dim, at)
         op, os_ = out.data_ptr(), q_heads * dim
     else:
         op, os_, _, n = _heads(out, q_heads, dim, q.dtype, index, "out")
@@ -312,7 +313,7 @@ def kv8_attention(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, scale: floa
     lp = None
     if lse is not None and lse is not False:
         if lse is True:
-            lse = _new(at, True, torch.empty, (rows, q_heads), dtype=torch.float32, device=cache.device)
+            lse = _dense(at, (rows, q_heads), torch.float32, cache.device)
         if tuple(_need(lse, torch.float32, 2, "lse").shape) != (rows, q_heads) or not lse.is_contiguous() or lse.get_device() != index:
             raise ValueError(f"lse must be a contiguous [{rows}][{q_heads}] on cuda:{index}")
         lp = lse.data_ptr()
@@ -320,7 +321,7 @@ def kv8_attention(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, scale: floa
     if workspace is None:
         wn = L.kv8_attention_workspace_bytes(cache._ref, batch._ref, q_heads, rows)
         if wn:
-            workspace = _new(at, False, torch.empty, wn, dtype=torch.uint8, device=cache.device)
+            workspace = _dense(at, wn, torch.uint8, cache.device, kept=False)
             wp = workspace.data_ptr()
     elif workspace.dtype != torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{index}")
@@ -356,14 +357,14 @@ def kv8_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, inv_fr
     qw, kw = _vector(q_weight, dim, torch.float32, index, "q_weight"), _vector(k_weight, dim, torch.float32, index, "k_weight")
     at = _place(index, stream)
     if q_out is None:
-        q_out = _new(at, True, _like, q, rows, q_heads, dim)
+        q_out = _like(q, rows, q_heads, dim, at)
         qop, qos = q_out.data_ptr(), q_heads * dim
     else:
         qop, qos, _, n = _heads(q_out, q_heads, dim, dtype, index, "q_out")
         if n != rows:
             raise ValueError(f"q_out must have {rows} rows")
     if k_out is None:
-        k_out = _new(at, True, _like, k, rows, k_heads, dim)
+        k_out = _like(k, rows, k_heads, dim, at)
         kop, kos = k_out.data_ptr(), k_heads * dim
     else:
         kop, kos, _, n = _heads(k_out, k_heads, dim, dtype, index, "k_out")
