@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Cache c, Batch s, cons
 }
 
 // Read-back, the inverse.  Bound by memory: 405 MB of codes and BF16 values in
-// 70 to 83 us (4.9 to 5.8 TB/s).
+// 78 to 85 us (4.8 to 5.2 TB/s).
 template <typename T, int kTokens>
 __global__ void __launch_bounds__(kThreads) read_kernel(Cache c, Batch s, T *__restrict__ ko, int64_t k_stride,
                                                         T *__restrict__ vo, int64_t v_stride, int waves, int64_t items) {
@@ -1046,10 +1046,10 @@ __device__ inline f16x8 codes_to_f16(int low, int high) {
 // loaded while the tile before it is weighted and multiplied by V, its V while
 // its own logits are formed, into the registers that the tile before has just
 // left; the pages are looked up one tile further ahead.  64 sequences of 500 to
-// 8000 tokens, 32 query heads over 8 of 128, BF16: 108 us for 559 MB (5.2 TB/s;
-// a read alone reaches 5.4 to 6.4).  A single sequence of 777 tokens takes 8.7
-// to 11 us, latency and the fetch of instructions, one of 65536 tokens and 2
-// heads 11 us (3.1 TB/s).  Eight waves, or two tiles on their way, were slower.
+// 8000 tokens, 32 query heads over 8 of 128, BF16: 115 us for 559 MB (4.9 TB/s;
+// a read alone reaches 5.4 to 6.4).  A single sequence of 777 tokens takes 11 us,
+// latency and the fetch of instructions, one of 65536 tokens and 2 heads 12 us
+// (2.9 TB/s).  Eight waves, or two tiles on their way, were slower.
 // kChunks: 64-component chunks of a head, kFull: the head fills them.
 template <typename T, int kChunks, bool kFull>
 __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_few_kernel(Attend a) {
@@ -1167,9 +1167,10 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_few_k
 // bytes, free of bank conflicts.  Bound by issuing vector instructions (a
 // weight's exponent, sum and f16 parts, the joining of digits) and the matrix
 // products, which a wave does by turns.  A causal prompt of 4096 F32 rows, 12
-// query heads over 2 of 128: 118 us, 0.44 PFLOP/s of the formula's operations.
-// Six BF16 prompts of 150 to 5000 tokens, 16 query heads over 4 of 64, a window
-// of 1024: 136 us, 0.49 PFLOP/s.
+// query heads over 2 of 128: 115 to 120 us, 0.44 PFLOP/s of the formula's
+// operations; vector instructions are active in 58% of the SIMDs' cycles, the
+// matrix units in 35%.  Six BF16 prompts of 150 to 5000 tokens, 16 query heads
+// over 4 of 64, a window of 1024: 139 us, 0.48 PFLOP/s; 76% and 19%.
 //
 // F32 rows by digits where 48 KB of codes and V leave room for a third
 // workgroup and f16 keys (64 KB) do not: one prompt of 4096 rows, 12 heads over
@@ -1651,15 +1652,15 @@ Plan plan_of(const Cache &c, const Batch &s, int64_t max_len, int64_t q_heads, i
   const int64_t held = static_cast<int64_t>(s.blocks) << c.lp;
   if (max_len <= 0 || max_len > held) max_len = held;
   // Over 26 calls each of 48 to 128, to 512 and of more rows a sequence, lengths
-  // drawn up to 4096 and beyond, the kernel for few rows took 1.31, 1.28 and 2.10
-  // times (floor + 8 us) in the mean, that for many 1.50, 1.48 and 1.75, the
-  // one of the lower estimate 1.32, 1.28 and 1.70.
+  // drawn up to 4096 and beyond, the kernel for few rows took 1.38, 1.27 and 1.97
+  // times (floor + 8 us) in the mean, that for many 1.37, 1.42 and 1.91, the
+  // one of the lower estimate 1.34, 1.26 and 1.69.
   Plan best = plan_for(0, c, s, max_len, q_heads);
   if (rows > 16) {
     // Two tiles of rows a wave read and turn V half as often, one leaves more
     // workgroups to balance: 16 heads of width 64, prompts of 150 to 5000
-    // tokens, 172 against 185 us; 12 heads of width 128, one prompt of 4096
-    // tokens in F32 (386 workgroups of two tiles), 176 against 122 us.
+    // tokens in BF16, 139 against 152 us; 12 heads of width 128, one prompt of
+    // 4096 tokens in F32 (386 workgroups of two tiles), 129 against 116 us.
     Plan many = plan_for(2, c, s, max_len, q_heads);
     if (c.dim > 128 || rows <= 64 || many.blocks * c.heads < 4 * kUnits) many = plan_for(1, c, s, max_len, q_heads);
     if (many.us < best.us) best = many;
