@@ -386,3 +386,52 @@ def test_few_bf16_rows_whose_values_cancel(D, P, lens, news):
     tol = ref["mag"] * (2 * weight + 2 * n * base.U + 2.0 ** -22)[..., None] + torch.finfo(BF16).eps / 2 * np.abs(ref["out"])
     assert tol.max() < 2.0 ** -14 * ref["mag"].max()
     assert (np.abs(out - ref["out"]) <= tol).all()
+
+
+# ---------------------------------------------------------------------------
+# Many rows beside bad ones, and captured
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("heads,D,P,group,lens,news,row_tiles", EXACT[2:] + [(1, 256, 64, 24, LONG, SHORT, 1)])
+def test_bad_queries_stay_in_their_rows_of_many(heads, D, P, group, lens, news, row_tiles, dtype):
+    w = World(80 + D, heads, D, P, lens, news)
+    q = w.values(w.rows, dtype, heads=heads * group, spread=0.0)
+    assert choice(w, heads * group, w.rows)[0] == row_tiles
+    clean = kv8.kv8_attention(w.cache, w.batch, base.dev(q, dtype))
+    hit = w.rng.random(q.shape[:2]) < 0.05
+    for row, head in zip(*np.nonzero(hit)):
+        q[row, head, w.rng.integers(D)] = w.rng.choice([np.nan, np.inf, -np.inf])
+    got, lse = kv8.kv8_attention(w.cache, w.batch, base.dev(q, dtype), lse=True)
+    a, b, s = base.host(clean), base.host(got), base.host(lse)
+    assert np.isnan(b[hit]).all() and np.isnan(s[hit]).all()
+    assert np.array_equal(a[~hit], b[~hit]) and np.isfinite(s[~hit]).all()
+
+
+def test_captured_calls_of_many_rows_and_on_a_forked_stream():
+    """Prompts split over the tokens, captured with the workspace of the
+    graph's own memory, and beside them a decode call on a stream that the
+    capture forks; replayed with other lengths and queries, eager calls between.
+    Every replay equals the eager calls bit for bit."""
+    w = World(91, 2, 128, 64, LONG, SHORT, blocks=-(-6000 // 64))
+    w.batch = kv8.KV8Batch(w.batch.table, w.batch.lens, w.batch.starts, max_len=6000)
+    assert choice(w, 32, w.rows) == (1, 2)
+    x, p = split_world(92)
+    lens = x.batch.lens
+    q = base.dev(w.values(w.rows, F16, heads=32), F16)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    kv8.kv8_attention(w.cache, w.batch, q), kv8.kv8_attention(x.cache, x.batch, p, stream=side)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        two = kv8.kv8_attention(x.cache, x.batch, p, lse=True, stream=side)
+        one = kv8.kv8_attention(w.cache, w.batch, q, lse=True)
+        torch.cuda.current_stream().wait_stream(side)
+    for turn in range(5):
+        lens.sub_(torch.tensor([100, 7], dtype=torch.int32, device=base.DEV))
+        w.batch.lens.sub_(1)
+        q.mul_(-0.9), p.mul_(-1.1)
+        graph.replay()
+        want = kv8.kv8_attention(w.cache, w.batch, q, lse=True) + kv8.kv8_attention(x.cache, x.batch, p, lse=True)
+        torch.cuda.synchronize()
+        for a, b in zip(one + two, want):
+            assert torch.equal(a, b)
