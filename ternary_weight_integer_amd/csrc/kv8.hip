@@ -568,8 +568,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Cache c, Batch s, T *__r
 //   O^T = V^T P^T  f16 16x16x32.  V's codes are exact in f16; a weight is the sum
 //     of two (22 bits), where many BF16 rows are worked on one (11 bits: its
 //     rounding is an eighth of the result's own, and adds 0.5 to 0.8% to its
-//     error; a second takes 18 to 20% of a prompt's time, and 0.7% where few rows
-//     wait for the cache).
+//     error; a second takes 18 to 20% of a prompt's time, and 1 to 4% where rows
+//     are few).
 // The rows of K's four 16-token operands are taken from the tile in the order
 // 16 (m / 4) + 4 j + m % 4, which leaves lane (row, g) with the logits of the
 // 16 consecutive tokens 16 g ..: those are its k indices of P^T, and one
