@@ -618,13 +618,17 @@ struct Attend {
 
 // What rounding x0 and x1 to the pair left, as a pair of its own: differences
 // that are exact, rounded once; one mixed-precision operation each (the compiler
-// takes three for two).
+// takes three for two).  It does not see what these write: settle() stands
+// between them and a matrix instruction, which may read a register two wait
+// states after another instruction wrote it.
 __device__ inline f16x2 rest_of(float x0, float x1, f16x2 pair) {
   f16x2 r;
   asm("v_fma_mixlo_f16 %0, %1, -1.0, %2 op_sel:[0,0,0] op_sel_hi:[1,0,0]" : "=v"(r) : "v"(pair), "v"(x0));
   asm("v_fma_mixhi_f16 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "+v"(r) : "v"(pair), "v"(x1));
   return r;
 }
+
+__device__ inline void settle(f16x8 &a, f16x8 &b) { asm("s_nop 1" : "+v"(a), "+v"(b)); }
 
 // What a tile of rows sees: tokens [begin, end), all of its rows [lo, hi), cut
 // into `used` parts of `part` token tiles.
@@ -991,6 +995,7 @@ struct Rows {
       w[0].pair[k / 2] = near;
       if constexpr (kParts == 2) w[1].pair[k / 2] = rest_of(p0, p1, near);
     }
+    if constexpr (kParts == 2) settle(w[1].half[0], w[1].half[1]);
     l[t] = fmaf(sum, rvs, l[t]);
   }
 
