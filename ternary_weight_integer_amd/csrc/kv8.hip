@@ -489,55 +489,8 @@ extern "C" int kv8_attention(const kv8_cache *cache, const kv8_batch *batch, int
                              int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
   Attend a;
   if (const int st = check_attention(cache, batch, type, q_heads, rows, a.c, a.s)) return st;
-  if (window < 0 || !(fabsf(scale) < INFINITY)) return I2S_EINVAL;
-  if (rows == 0 || a.s.seqs == 0) return I2S_OK;
-  const int64_t width = q_heads * a.c.dim;
-  if (const int st = check_rows(q, q_stride, width, value_bytes(type))) return st;
-  if (const int st = check_rows(out, out_stride, width, value_bytes(type))) return st;
-  if (!aligned(lse, 4)) return I2S_EINVAL;
-  const Plan p = plan_of(a.c, a.s, batch->max_len, q_heads, window_of(window), causal != 0);
-  if (p.blocks * a.c.heads * p.splits > 0x7fffffff || rows * q_heads > 0x7fffffff) return I2S_ERANGE;
-  const size_t need = workspace_of(p, a.c, a.s, q_heads);
-  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return I2S_EWORKSPACE;
-  a.q = q;
-  a.out = out;
-  a.lse = lse;
-  a.acc = static_cast<float *>(workspace);
-  a.ml = need ? a.acc + static_cast<int64_t>(p.splits) * rows * q_heads * a.c.dim : nullptr;
-  a.q_stride = q_stride;
-  a.out_stride = out_stride;
-  a.window = static_cast<int>(window_of(window));
-  a.scale = scale * 1.44269504088896341f;
-  a.q_heads = static_cast<int>(q_heads);
-  a.group = static_cast<int>(q_heads / a.c.heads);
-  a.causal = causal != 0;
-  a.by_group = Divisor(a.group);
-  a.by_splits = Divisor(p.splits);
-  a.by_heads = Divisor(a.q_heads);
-  a.by_per_seq = Divisor(a.s.per_seq > 0 ? a.s.per_seq : 1);
-  const int64_t each = (a.s.per_seq * static_cast<int64_t>(a.group) + p.block_rows - 1) / p.block_rows;
-  a.by_each = Divisor(each > 0 ? static_cast<int>(each) : 1);
-  a.splits = p.splits;
-  a.least = p.least;
-  a.blocks = static_cast<int>(p.blocks);
-  a.round = kUnits / (a.c.heads * p.splits) > 1 ? kUnits / (a.c.heads * p.splits) : 1;
-  a.by_round = Divisor(a.round);
-  const hipStream_t on = static_cast<hipStream_t>(stream);
-  return by_type(type, [&](auto t) {
-    typedef decltype(t) T;
-    const int st = a.c.dim == 128  ? launch_attention<T, 2, true>(p, a, on)
-                   : a.c.dim == 64 ? launch_attention<T, 1, true>(p, a, on)
-                   : a.c.dim < 64  ? launch_attention<T, 1, false>(p, a, on)
-                   : a.c.dim < 128 ? launch_attention<T, 2, false>(p, a, on)
-                                   : launch_attention<T, 4, false>(p, a, on);
-    if (st || p.splits == 1) return st;
-    if (p.splits > kFewParts) {
-      join_many_kernel<T><<<dim3(static_cast<unsigned>(rows), a.q_heads), kThreads, 0, on>>>(a, p.block_rows);
-    } else {
-      join_few_kernel<T><<<static_cast<unsigned>((rows * q_heads + 7) / 8), kThreads, 0, on>>>(a, p.block_rows);
-    }
-    return hip_status();
-  });
+  const Rowset r = {q, q_stride, q_heads, rows, out, out_stride, lse, workspace, workspace_bytes};
+  return attend(a, batch, type, r, scale, causal, window, stream);
 }
 
 extern "C" int kv8_qk_norm_rope(int type, int64_t rows, int64_t dim, const void *q, int64_t q_stride, int64_t q_heads,

@@ -55,6 +55,7 @@ constexpr float kMinScale = 1e-20f;
 constexpr float kNothing = 127.5f * kMinScale;
 constexpr int kTile = 64;          // tokens
 constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLog2e = 1.44269504088896341f;
 constexpr int kMaxSplits = 256;
 constexpr int kFewParts = 8;       // that 32 lanes join
 
@@ -72,6 +73,20 @@ struct Attend {
   Divisor by_group, by_splits, by_round, by_each, by_heads, by_per_seq;  // by_each: workgroups of a sequence, starts NULL
   int blocks, round;  // workgroups along the rows of one head and part, and those that fill the compute units once
 };
+
+// A call whose scores have a shape of their own: capped (in units of log2: at
+// `cap`, icap = 1 / cap; 0: not), with a bias by distance (slopes NULL: none),
+// with a prefix that all rows see (prefix NULL: none).  Kernels are built for
+// either argument: to those of plain scores the shape costs nothing.
+struct Shaped : Attend {
+  float cap, icap;
+  const float *slopes;    // [q_heads]
+  const int32_t *prefix;  // [seqs]
+};
+
+// Tokens in front of which rows of sequence b see all.
+__device__ inline int prefix_of(const Attend &, int) { return 0; }
+__device__ inline int prefix_of(const Shaped &a, int b) { return a.prefix ? a.prefix[b] : 0; }
 
 // What rounding x0 and x1 to the pair left, as a pair of its own: differences
 // that are exact, rounded once; one mixed-precision operation each (the compiler
@@ -97,12 +112,22 @@ constexpr int kLeastFew = 8, kLeastMany = 4;  // token tiles of a part: shorter 
 
 __device__ inline int clamp_int(int64_t v, int top) { return v < 0 ? 0 : v < top ? static_cast<int>(v) : top; }
 
-__device__ inline Range range_of(const Attend &a, const Span &p, int first_row, int last_row) {
+// The end of what a row at position pos sees, at most top.
+template <typename A>
+__device__ inline int end_of(const A &a, int pos, int prefix, int top) {
+  int64_t end = static_cast<int64_t>(pos) + 1;
+  if constexpr (std::is_same<A, Shaped>::value) end = end > prefix ? end : prefix;
+  return a.causal ? clamp_int(end, top) : top;
+}
+
+template <typename A>
+__device__ inline Range range_of(const A &a, const Span &p, int first_row, int last_row) {
   const int ahead = p.len - p.n, p0 = ahead + a.by_group.of(first_row), p1 = ahead + a.by_group.of(last_row);
   const int held = a.s.blocks << a.c.lp, top = held < p.len ? held : p.len;
   Range r;
-  r.hi = a.causal ? clamp_int(static_cast<int64_t>(p0) + 1, top) : top;
-  r.end = a.causal ? clamp_int(static_cast<int64_t>(p1) + 1, top) : top;
+  const int prefix = prefix_of(a, p.b);
+  r.hi = end_of(a, p0, prefix, top);
+  r.end = end_of(a, p1, prefix, top);
   r.lo = a.window > 0 ? clamp_int(static_cast<int64_t>(p1) - a.window + 1, top) : 0;
   r.begin = (a.window > 0 ? clamp_int(static_cast<int64_t>(p0) - a.window + 1, top) : 0) & ~(kTile - 1);
   const int tiles = r.end > r.begin ? (r.end - r.begin + kTile - 1) / kTile : 0;
@@ -124,6 +149,39 @@ __device__ inline float over_lanes_sum(float v) {
   v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
   auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// a - b, held to the range of an int.
+__device__ inline int sub_sat(int a, int b) { return __builtin_elementwise_sub_sat(a, b); }
+
+// cap tanh(x / cap) of 16 scores, with icap = 1 / cap.  Up to kBend x / cap is
+// a polynomial, which scores below 5/8 of the cap need no more of (a branch of
+// the wave): tanh(y) = y + y z Q(z), z = y^2, Q fitted to a relative error of
+// 2^-27.9 (least squares at Chebyshev nodes, reweighted to even it out), so that
+// x itself is only rounded once more.  Above: (1 - u) / (1 + u), u = exp(-2 |y|).
+constexpr float kBend = 0.625f;
+
+__device__ inline void capped(float (&x)[16], float cap, float icap) {
+  float most = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) most = fmaxf(most, fabsf(x[k]));
+  const bool far = __any(most * icap > kBend);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float y = x[k] * icap, z = y * y;
+    float q = fmaf(z, -0x1.72eedap-8f, 0x1.515cdep-6f);
+    q = fmaf(q, z, -0x1.b8153ep-5f);
+    q = fmaf(q, z, 0x1.110580p-3f);
+    q = fmaf(q, z, -0x1.555524p-2f);
+    const float near = fmaf(x[k], z * q, x[k]);
+    if (far) {
+      const float u = __builtin_amdgcn_exp2f(fabsf(y) * (-2.0f * kLog2e));
+      const float wide = copysignf(cap * ((1.0f - u) * __builtin_amdgcn_rcpf(1.0f + u)), y);
+      x[k] = fabsf(y) > kBend ? wide : near;
+    } else {
+      x[k] = near;
+    }
+  }
 }
 
 // Four codes as f16: 0x6400 + u is 1024 + u for a byte u = code + 128.
@@ -244,8 +302,9 @@ struct Scales {
 // A wave's rows: queries, running statistics, results.  Lane (n, g) holds row
 // n of each row tile; of a tile of tokens its logits are those of the 16
 // tokens 16 g .., of a result the components 16 d + 4 g ...
-template <typename T, int kChunks, bool kFull, int kRowTiles, bool kDirect, int kWeightParts>
+template <typename A, typename T, int kChunks, bool kFull, int kRowTiles, bool kDirect, int kWeightParts>
 struct Rows {
+  static constexpr bool kShaped = std::is_same<A, Shaped>::value;
   static constexpr int kDigits = 4, kHalves = 2;
   static constexpr int kTerms = std::is_same<T, float>::value ? 2 : 1;    // f16 terms of a query's component
   static constexpr int kOperands = kDirect ? kHalves * kTerms : kDigits;  // of 64 components of the queries
@@ -259,7 +318,7 @@ struct Rows {
     f16x8 half[2];
   };
 
-  const Attend &a;
+  const A &a;
   const int n, g, D;
   f32x4 acc[kRowTiles][kOut];
   i32x4 q[kRowTiles][kChunks][kOperands];
@@ -267,11 +326,14 @@ struct Rows {
   int lo[kRowTiles], hi[kRowTiles];
   int row_of[kRowTiles], head_of[kRowTiles];        // row_of: -1 behind the last row
   Vec qv[kRowTiles][kChunks][kVecs];
+  float slope[kShaped ? kRowTiles : 1];  // in units of log2
+  int pos_of[kShaped ? kRowTiles : 1];
 
-  __device__ Rows(const Attend &args)
+  __device__ Rows(const A &args)
       : a(args), n(threadIdx.x & 15), g((threadIdx.x & 63) >> 4), D(kFull ? 64 * kChunks : args.c.dim) {}
 
   __device__ void place(const Place &w, int row0, int end) {
+    const int prefix = prefix_of(a, w.p.b);
 #pragma unroll
     for (int t = 0; t < kRowTiles; ++t) {
       const int row = row0 + 16 * t + n;
@@ -280,7 +342,11 @@ struct Rows {
       const int pos = w.p.len - w.p.n + i;
       row_of[t] = live ? w.p.first + i : -1;
       head_of[t] = w.h * a.group + (live ? row - i * a.group : 0);
-      hi[t] = !live ? 0 : a.causal ? clamp_int(static_cast<int64_t>(pos) + 1, end) : end;
+      hi[t] = !live ? 0 : end_of(a, pos, prefix, end);
+      if constexpr (kShaped) {
+        slope[t] = a.slopes ? a.slopes[head_of[t]] * kLog2e : 0.0f;
+        pos_of[t] = pos;
+      }
       lo[t] = a.window > 0 ? clamp_int(static_cast<int64_t>(pos) - a.window + 1, end) : 0;
       qs[t] = 0.0f;
       m[t] = kNoMax;
@@ -400,9 +466,29 @@ struct Rows {
   // running statistics.  edge: some row of the wave does not see them all, or
   // some are in a hole.
   __device__ void weigh(int t, const f32x4 (&f)[4], const Scales &s, int first, bool edge, Weights (&w)[kParts]) {
+    if constexpr (kShaped) {
+      float x[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] = f[k / 4][k % 4] * (qs[t] * s.ks);
+      if (a.cap > 0.0f) capped(x, a.cap, a.icap);
+      if (a.slopes) {
+        const float away = static_cast<float>(sub_sat(pos_of[t], first));
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] = fmaf(-slope[t], fabsf(away - static_cast<float>(k)), x[k]);
+      }
+      f32x4 e[4];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) e[k / 4][k % 4] = x[k];
+      weigh_scaled(t, e, 1.0f, s, first, edge, w);
+    } else {
+      weigh_scaled(t, f, qs[t] * s.ks, s, first, edge, w);
+    }
+  }
+
+  // The same for scores f * ck in units of log2.
+  __device__ void weigh_scaled(int t, const f32x4 (&f)[4], float ck, const Scales &s, int first, bool edge, Weights (&w)[kParts]) {
     const float vs = s.hole ? 1.0f : fmaxf(s.vs, kMinScale);
     const float lvs = __builtin_amdgcn_logf(vs), rvs = __builtin_amdgcn_rcpf(vs);
-    const float ck = qs[t] * s.ks;
     // Taken off the exponents: the running maximum, nothing while there is none.
     const bool unset = m[t] == kNoMax;
     const float off = unset ? 0.0f : m[t];
@@ -513,9 +599,9 @@ __device__ inline f16x8 codes_to_f16(int low, int high) {
 // latency and the fetch of instructions, one of 65536 tokens and 2 heads 12 us
 // (2.9 TB/s).  Eight waves, or two tiles on their way, were slower.
 // kChunks: 64-component chunks of a head, kFull: the head fills them.
-template <typename T, int kChunks, bool kFull>
-__global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_few_kernel(Attend a) {
-  typedef Rows<T, kChunks, kFull, 1, false, 2> R;
+template <typename A, typename T, int kChunks, bool kFull>
+__global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) attention_few_kernel(A a) {
+  typedef Rows<A, T, kChunks, kFull, 1, false, 2> R;
   constexpr int kOut = R::kOut, kWaves = kThreads / 64, kStep = kWaves * kTile;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   Place w;
@@ -645,10 +731,10 @@ struct Many {
   static constexpr int kGroups = kChunks > 2 ? 1 : kDirect ? 2 : 3;  // workgroups on a unit, at least
 };
 
-template <typename T, int kChunks, bool kFull, int kRowTiles>
-__global__ void __launch_bounds__(kThreads, (Many<T, kChunks, kRowTiles>::kGroups)) attention_many_kernel(Attend a) {
+template <typename A, typename T, int kChunks, bool kFull, int kRowTiles>
+__global__ void __launch_bounds__(kThreads, (Many<T, kChunks, kRowTiles>::kGroups)) attention_many_kernel(A a) {
   constexpr bool kDirect = Many<T, kChunks, kRowTiles>::kDirect;
-  typedef Rows<T, kChunks, kFull, kRowTiles, kDirect, std::is_same<T, bf16>::value ? 1 : 2> R;
+  typedef Rows<A, T, kChunks, kFull, kRowTiles, kDirect, std::is_same<T, bf16>::value ? 1 : 2> R;
   constexpr int kOut = R::kOut, kRows = 16 * kRowTiles, kBlock = 4 * kRows;
   __shared__ i32x4 lk[2][4][kChunks][R::kKeys][64];
   __shared__ f16x8 lv[2][kOut][2][64];
@@ -790,7 +876,8 @@ __global__ void __launch_bounds__(kThreads, (Many<T, kChunks, kRowTiles>::kGroup
 // Joins the parts of rows that were split.
 
 // The parts that the row and head at place `at` was cut into.
-__device__ inline int parts_of(const Attend &a, const Span &p, int row, int hq, int block_rows) {
+template <typename A>
+__device__ inline int parts_of(const A &a, const Span &p, int row, int hq, int block_rows) {
   const int h = a.by_group.of(hq), in_group = (row - p.first) * a.group + hq - h * a.group;
   const int row0 = in_group & -block_rows;  // a power of two
   const int rows = p.n * a.group;
@@ -799,8 +886,8 @@ __device__ inline int parts_of(const Attend &a, const Span &p, int row, int hq, 
 
 // Few parts (at most kFewParts): 32 lanes a row and head, four components each.
 // block_rows: rows of the attention's workgroups.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) join_few_kernel(Attend a, int block_rows) {
+template <typename A, typename T>
+__global__ void __launch_bounds__(kThreads) join_few_kernel(A a, int block_rows) {
   const int each = a.s.rows * a.q_heads, item = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int row = a.by_heads.of(item < each ? item : each - 1), hq = item - row * a.q_heads, D = a.c.dim;
   // A wave's two items may lie in neighbouring rows, and these in two sequences
@@ -848,8 +935,8 @@ __global__ void __launch_bounds__(kThreads) join_few_kernel(Attend a, int block_
 
 // Many parts: a workgroup a row and head; its threads hold the parts' weights,
 // and eight groups of 32 lanes each sum every eighth part.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) join_many_kernel(Attend a, int block_rows) {
+template <typename A, typename T>
+__global__ void __launch_bounds__(kThreads) join_many_kernel(A a, int block_rows) {
   static_assert(kMaxSplits == kThreads, "a thread holds one part's weight");
   __shared__ f32x4 sums[8][KV8_MAX_DIM / 4];
   __shared__ float weight[kMaxSplits], red[4], sl[4];
@@ -978,16 +1065,82 @@ inline size_t workspace_of(const Plan &p, const Cache &c, const Batch &s, int64_
   return p.splits > 1 ? static_cast<size_t>(p.splits) * s.rows * q_heads * (c.dim + 2) * sizeof(float) : 0;
 }
 
-template <typename T, int kChunks, bool kFull>
-int launch_attention(const Plan &p, const Attend &a, hipStream_t stream) {
+template <typename T, int kChunks, bool kFull, typename A>
+int launch_attention(const Plan &p, const A &a, hipStream_t stream) {
   const unsigned grid = static_cast<unsigned>(p.blocks * a.c.heads * p.splits);
   if (p.row_tiles == 0) {
-    attention_few_kernel<T, kChunks, kFull><<<grid, kThreads, 0, stream>>>(a);
+    attention_few_kernel<A, T, kChunks, kFull><<<grid, kThreads, 0, stream>>>(a);
   } else if (p.row_tiles == 1) {
-    attention_many_kernel<T, kChunks, kFull, 1><<<grid, kThreads, 0, stream>>>(a);
+    attention_many_kernel<A, T, kChunks, kFull, 1><<<grid, kThreads, 0, stream>>>(a);
   } else if constexpr (kChunks <= 2) {  // two row tiles fit the registers, see plan_of
-    attention_many_kernel<T, kChunks, kFull, 2><<<grid, kThreads, 0, stream>>>(a);
+    attention_many_kernel<A, T, kChunks, kFull, 2><<<grid, kThreads, 0, stream>>>(a);
   }
   return hip_status();
 }
+
+// Rows, outputs and workspace of a call.
+struct Rowset {
+  const void *q;
+  int64_t q_stride, q_heads, rows;
+  void *out;
+  int64_t out_stride;
+  float *lse;
+  void *workspace;
+  size_t workspace_bytes;
+};
+
+// The call itself: what is left to check, the plan and the launches.
+template <typename A>
+int attend(A &a, const kv8_batch *batch, int type, const Rowset &r, float scale, int causal, int64_t window, void *stream) {
+  if (window < 0 || !(fabsf(scale) < INFINITY)) return I2S_EINVAL;
+  if (r.rows == 0 || a.s.seqs == 0) return I2S_OK;
+  const int64_t width = r.q_heads * a.c.dim;
+  if (const int st = check_rows(r.q, r.q_stride, width, value_bytes(type))) return st;
+  if (const int st = check_rows(r.out, r.out_stride, width, value_bytes(type))) return st;
+  if (!aligned(r.lse, 4)) return I2S_EINVAL;
+  const Plan p = plan_of(a.c, a.s, batch->max_len, r.q_heads, window_of(window), causal != 0);
+  if (p.blocks * a.c.heads * p.splits > 0x7fffffff || r.rows * r.q_heads > 0x7fffffff) return I2S_ERANGE;
+  const size_t need = workspace_of(p, a.c, a.s, r.q_heads);
+  if (need > 0 && (!r.workspace || r.workspace_bytes < need || !aligned(r.workspace, 256))) return I2S_EWORKSPACE;
+  a.q = r.q;
+  a.out = r.out;
+  a.lse = r.lse;
+  a.acc = static_cast<float *>(r.workspace);
+  a.ml = need ? a.acc + static_cast<int64_t>(p.splits) * r.rows * r.q_heads * a.c.dim : nullptr;
+  a.q_stride = r.q_stride;
+  a.out_stride = r.out_stride;
+  a.window = static_cast<int>(window_of(window));
+  a.scale = scale * kLog2e;
+  a.q_heads = static_cast<int>(r.q_heads);
+  a.group = static_cast<int>(r.q_heads / a.c.heads);
+  a.causal = causal != 0;
+  a.by_group = Divisor(a.group);
+  a.by_splits = Divisor(p.splits);
+  a.by_heads = Divisor(a.q_heads);
+  a.by_per_seq = Divisor(a.s.per_seq > 0 ? a.s.per_seq : 1);
+  const int64_t each = (a.s.per_seq * static_cast<int64_t>(a.group) + p.block_rows - 1) / p.block_rows;
+  a.by_each = Divisor(each > 0 ? static_cast<int>(each) : 1);
+  a.splits = p.splits;
+  a.least = p.least;
+  a.blocks = static_cast<int>(p.blocks);
+  a.round = kUnits / (a.c.heads * p.splits) > 1 ? kUnits / (a.c.heads * p.splits) : 1;
+  a.by_round = Divisor(a.round);
+  const hipStream_t on = static_cast<hipStream_t>(stream);
+  return by_type(type, [&](auto t) {
+    typedef decltype(t) T;
+    const int st = a.c.dim == 128  ? launch_attention<T, 2, true>(p, a, on)
+                   : a.c.dim == 64 ? launch_attention<T, 1, true>(p, a, on)
+                   : a.c.dim < 64  ? launch_attention<T, 1, false>(p, a, on)
+                   : a.c.dim < 128 ? launch_attention<T, 2, false>(p, a, on)
+                                   : launch_attention<T, 4, false>(p, a, on);
+    if (st || p.splits == 1) return st;
+    if (p.splits > kFewParts) {
+      join_many_kernel<A, T><<<dim3(static_cast<unsigned>(r.rows), a.q_heads), kThreads, 0, on>>>(a, p.block_rows);
+    } else {
+      join_few_kernel<A, T><<<static_cast<unsigned>((r.rows * r.q_heads + 7) / 8), kThreads, 0, on>>>(a, p.block_rows);
+    }
+    return hip_status();
+  });
+}
+
 }  // namespace
