@@ -299,36 +299,49 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) weigh_kernel(We
   }
 }
 
-// Joins the parts of token blocks that were split: a workgroup a block.
+// Joins the parts of token blocks that were split: a workgroup has 64 tokens, 16
+// teams of 16 lanes sum every 16th part (a thread a token and all parts in turn
+// took 19 us for a prompt of 4096, 64 parts).
+constexpr int kJoinTokens = 64, kTeams = 16;
+
 __global__ void __launch_bounds__(kThreads) weigh_join_kernel(Weigh a) {
-  const int rest = a.c.by_heads.of(blockIdx.x), h = blockIdx.x - rest * a.c.heads;
-  const int b = a.by_blocks.of(rest), block = rest - b * a.blocks;
+  __shared__ f32x4 sum[kTeams][kJoinTokens / 4];
+  const int h = blockIdx.x % a.c.heads, x = blockIdx.x / a.c.heads;
+  constexpr int kPer = kBlockTokens / kJoinTokens;
+  const int b = a.by_blocks.of(x / kPer), block = x / kPer - b * a.blocks;
   const Span p = span_of(a.s, b);
   const int64_t held = static_cast<int64_t>(a.s.blocks) << a.c.lp;
-  const int top = held < p.len ? static_cast<int>(held) : p.len, t0 = block * kBlockTokens, t = t0 + threadIdx.x;
-  if (p.n == 0 || t >= top) return;
+  const int top = held < p.len ? static_cast<int>(held) : p.len, t0 = block * kBlockTokens, part0 = x % kPer * kJoinTokens;
+  if (p.n == 0 || t0 + part0 >= top) return;
   const Passing r = passing(a, p, t0, t0 + kBlockTokens < top ? t0 + kBlockTokens : top, true);
   if (r.stages <= r.each) return;
-  const int page = page_of(a.s, b, t >> a.c.lp, a.c.pages);
-  if (page < 0) return;
+  const int team = threadIdx.x >> 4, lane = threadIdx.x & 15, used = (r.stages + r.each - 1) / r.each;
   const int64_t all = static_cast<int64_t>(a.s.seqs) * a.c.heads * a.blocks;
-  const float *at = a.sums + ((static_cast<int64_t>(b) * a.c.heads + h) * a.blocks + block) * kBlockTokens + threadIdx.x;
-  float w = 0.0f;
-  for (int k = 0; k * r.each < r.stages; ++k) w += at[k * all * kBlockTokens];
-  settle_mass(a, page, h, t, t >= p.len - p.n, w);
+  const float *at = a.sums + ((static_cast<int64_t>(b) * a.c.heads + h) * a.blocks + block) * kBlockTokens + part0 + 4 * lane;
+  f32x4 w = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int k = team; k < used; k += kTeams) w += *reinterpret_cast<const f32x4 *>(at + k * all * kBlockTokens);
+  sum[team][lane] = w;
+  __syncthreads();
+  if (threadIdx.x >= kJoinTokens) return;
+  const int t = t0 + part0 + threadIdx.x;
+  const int page = t < top ? page_of(a.s, b, t >> a.c.lp, a.c.pages) : -1;
+  float v = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kTeams; ++k) v += reinterpret_cast<const float *>(sum[k])[threadIdx.x];
+  if (page >= 0) settle_mass(a, page, h, t, t >= p.len - p.n, v);
 }
 
 // ---------------------------------------------------------------------------
 // The choice of the tokens that stay.
 
-constexpr int kChooseThreads = 1024, kBins = 256;
+constexpr int kChooseThreads = 1024, kChooseWaves = kChooseThreads / 64, kBins = 2048;
 
 struct Choose {
   Cache c;
   Batch s;
   const float *mass;
-  int64_t keep;
-  int first, recent;
+  int keep, first, recent;
   int32_t *index, *kept;
 };
 
@@ -341,68 +354,165 @@ __device__ inline uint32_t rank_of(float mass, bool always) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// A workgroup has a sequence and head.  The least rank that stays is found
-// digit by digit from the highest, with a histogram of the ranks that begin with
-// the digits found; then the tokens are written in order.
+// Sum over the wave's lanes up to this one.
+__device__ inline int wave_scan(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int k = 1; k < 64; k *= 2) {
+    const int other = __shfl_up(v, k);
+    v += lane >= k ? other : 0;
+  }
+  return v;
+}
+
+// A workgroup has a sequence and head, a lane four neighbouring tokens of each
+// of kLoads rounds, whose ranks stay in registers; a sequence of more tokens is
+// walked in segments, each pass again.  The least rank that stays is found in
+// digits of 11, 11 and 10 bits from the highest, with a histogram of the ranks
+// that begin with the digits found; then the tokens are written in order.
+template <int kLoads>
 __global__ void __launch_bounds__(kChooseThreads) choose_kernel(Choose a) {
-  __shared__ int hist[kBins], waves[2][kChooseThreads / 64];
-  const int h = blockIdx.x % a.c.heads, b = blockIdx.x / a.c.heads, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const Span p = span_of(a.s, b);
+  constexpr int kSegment = kLoads * kChooseThreads * 4;
+  typedef float F4 __attribute__((ext_vector_type(4), aligned(4)));
+  __shared__ int hist[kBins], waves[kChooseWaves], pick[2];
+  __shared__ int base[2][kLoads * kChooseWaves];
+  const int b = a.c.by_heads.of(blockIdx.x), h = blockIdx.x - b * a.c.heads;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int length = a.s.lens[b];
   const int64_t held = static_cast<int64_t>(a.s.blocks) << a.c.lp;
-  const int top = held < p.len ? static_cast<int>(held) : p.len;
-  auto rank = [&](int64_t t) -> uint32_t {
-    if (t >= top) return 0;
-    const int page = page_of(a.s, b, t >> a.c.lp, a.c.pages);
-    if (page < 0) return 0;
-    const int64_t at = static_cast<int64_t>(page) * a.c.heads + h;
-    return rank_of(a.mass[(at << a.c.lp) + (t & ((1 << a.c.lp) - 1))], t < a.first || t >= static_cast<int64_t>(p.len) - a.recent);
+  const int top = length <= 0 ? 0 : held < length ? static_cast<int>(held) : length;
+  const int newest = length - a.recent;  // tokens from here on stay
+  const int segments = top > 0 ? (top - 1) / kSegment + 1 : 0;
+  uint32_t rank[kLoads][4];
+  auto load = [&](int segment) {
+    const int begin = segment * kSegment + 4 * tid;
+    int entry[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int64_t t = begin + static_cast<int64_t>(i) * (4 * kChooseThreads);
+      entry[i] = a.s.table[b * a.s.table_stride + ((t < top ? t : top - 1) >> a.c.lp)];
+    }
+    F4 m[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int page = static_cast<unsigned>(entry[i]) < static_cast<unsigned>(a.c.pages) ? entry[i] : 0;
+      const int slot = (begin + i * (4 * kChooseThreads)) & ((1 << a.c.lp) - 1);
+      m[i] = *reinterpret_cast<const F4 *>(a.mass + ((static_cast<int64_t>(page) * a.c.heads + h) << a.c.lp) + slot);
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const bool hole = static_cast<unsigned>(entry[i]) >= static_cast<unsigned>(a.c.pages);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t t = begin + static_cast<int64_t>(i) * (4 * kChooseThreads) + k;
+        rank[i][k] = hole || t >= top ? 0 : rank_of(m[i][k], t < a.first || t >= newest);
+      }
+    }
   };
+
   uint32_t least = 0;
-  int64_t want = a.keep;  // of the ranks that begin with least's digits
-  int total = 0;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < kBins) hist[tid] = 0;
+  int want = a.keep, total = 0;  // want: of the ranks that begin with least's digits
+  if (segments == 1) load(0);
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    constexpr int kShift[3] = {21, 10, 0}, kAbove[3] = {32, 21, 10};
+    hist[tid] = 0;
+    hist[tid + kChooseThreads] = 0;
     __syncthreads();
-    for (int64_t t = tid; t < top; t += kChooseThreads) {
-      const uint32_t r = rank(t);
-      if (r != 0 && (shift == 24 || (r >> (shift + 8)) == (least >> (shift + 8)))) atomicAdd(&hist[(r >> shift) & (kBins - 1)], 1);
+    for (int segment = 0; segment < segments; ++segment) {
+      if (segments > 1) load(segment);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t r = rank[i][k];
+          const bool in = pass == 0 ? r != 0 : (r >> kAbove[pass]) == (least >> kAbove[pass]);
+          if (in) atomicAdd(&hist[(r >> kShift[pass]) & (pass == 2 ? 1023 : kBins - 1)], 1);
+        }
+      }
     }
     __syncthreads();
-    if (shift == 24)
-      for (int i = 0; i < kBins; ++i) total += hist[i];
-    if (total <= a.keep) break;
-    int digit = kBins - 1;
-    while (digit > 0 && hist[digit] < want) want -= hist[digit--];
-    least |= static_cast<uint32_t>(digit) << shift;
+    // Bins from the highest: a thread has two.
+    const int high = hist[kBins - 1 - 2 * tid], low = hist[kBins - 2 - 2 * tid];
+    int upto = wave_scan(high + low);
+    if (lane == 63) waves[wave] = upto;
     __syncthreads();
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < kChooseWaves; ++i) {
+      upto += i < wave ? waves[i] : 0;
+      sum += waves[i];
+    }
+    if (pass == 0) {
+      total = sum;
+      if (total <= a.keep) break;
+    }
+    const int before = upto - high - low;
+    if (before < want && want <= upto) {
+      const bool in_high = want <= before + high;
+      pick[0] = kBins - 1 - 2 * tid - (in_high ? 0 : 1);
+      pick[1] = want - before - (in_high ? 0 : high);
+    }
+    __syncthreads();
+    least |= static_cast<uint32_t>(pick[0]) << kShift[pass];
+    want = pick[1];
   }
   const bool all = total <= a.keep;
+  if (all) least = 1, want = total;  // every token, those of rank 1 in order
   int32_t *out = a.index + (static_cast<int64_t>(b) * a.c.heads + h) * a.keep;
-  int done = 0, ties = 0;
-  for (int64_t t0 = 0; t0 < top; t0 += kChooseThreads) {
-    const uint32_t r = rank(t0 + tid);
-    const bool tie = !all && r != 0 && r == least;
-    const uint64_t same = __ballot(tie), below = (uint64_t{1} << lane) - 1;
-    if (lane == 0) waves[0][wave] = __popcll(same);
-    __syncthreads();
-    int before = ties;
-    for (int i = 0; i < kChooseThreads / 64; ++i) {
-      before += i < wave ? waves[0][i] : 0;
-      ties += waves[0][i];
+  int done = 0, ties = 0;  // tokens over the least rank and at it, of earlier segments
+  const uint64_t below = (uint64_t{1} << lane) - 1;
+  for (int segment = 0; segment < segments && a.keep > 0; ++segment) {
+    if (segments > 1) load(segment);
+    __syncthreads();  // base has been read
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      int over = 0, at = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        over += __popcll(__ballot(rank[i][k] > least));
+        at += __popcll(__ballot(rank[i][k] == least));
+      }
+      if (lane == 0) {
+        base[0][i * kChooseWaves + wave] = over;
+        base[1][i * kChooseWaves + wave] = at;
+      }
     }
-    const bool stays = r != 0 && (all || r > least || (tie && before + __popcll(same & below) < want));
-    const uint64_t mine = __ballot(stays);
-    if (lane == 0) waves[1][wave] = __popcll(mine);
     __syncthreads();
-    int place = done;
-    for (int i = 0; i < kChooseThreads / 64; ++i) {
-      place += i < wave ? waves[1][i] : 0;
-      done += waves[1][i];
+    if (wave < 2) {  // sums in front of each
+      int carry = wave == 0 ? done : ties;
+      for (int i = 0; i < kLoads * kChooseWaves; i += 64) {
+        const bool in = i + lane < kLoads * kChooseWaves;
+        const int v = in ? base[wave][i + lane] : 0, upto = wave_scan(v);
+        if (in) base[wave][i + lane] = carry + upto - v;
+        carry += __builtin_amdgcn_readlane(upto, 63);
+      }
+      if (lane == 0) pick[wave] = carry;
     }
-    if (stays) out[place + __popcll(mine & below)] = static_cast<int32_t>(t0 + tid);
+    __syncthreads();
+    done = pick[0];
+    ties = pick[1];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      int over = base[0][i * kChooseWaves + wave], at = base[1][i * kChooseWaves + wave];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        over += __popcll(__ballot(rank[i][k] > least) & below);
+        at += __popcll(__ballot(rank[i][k] == least) & below);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t r = rank[i][k];
+        if (r > least || (r == least && at < want))
+          out[over + (at < want ? at : want)] = segment * kSegment + i * (4 * kChooseThreads) + 4 * tid + k;
+        over += r > least;
+        at += r == least;
+      }
+    }
   }
-  for (int64_t i = done + tid; i < a.keep; i += kChooseThreads) out[i] = -1;
-  if (h == 0 && tid == 0) a.kept[b] = done;
+  const int kept = all ? total : a.keep;
+  for (int i = kept + tid; i < a.keep; i += kChooseThreads) out[i] = -1;
+  if (h == 0 && tid == 0) a.kept[b] = kept;
 }
 
 // ---------------------------------------------------------------------------
@@ -412,52 +522,160 @@ struct Move {
   Cache c;
   Batch s;
   const int32_t *index, *kept, *to;
-  int64_t keep, to_stride;
-  int to_blocks, blocks;  // blocks: page slots of a sequence in the grid
+  int64_t to_stride, items;
+  int keep, to_blocks, blocks, waves;  // blocks: pages of a sequence in the grid; waves of an item
   float *mass;
+  Divisor by_blocks, by_units;  // units: 16 bytes of a token's key
 };
 
-// A workgroup has a page, a head, and K or V.
+constexpr int kMoveUnits = 2, kMoveBytes = 32;  // of a lane at a time
+
+// An item is a page to fill, a head, and K or V.  Keys are gathered 16 bytes a
+// lane; of V, tokens innermost, a lane has one token and takes its components
+// byte by byte: neighbouring lanes' tokens rise, so a wave's bytes of one
+// component lie in the few lines that these tokens span.  kOnce: the item's
+// codes stay in registers between the maximum and the new codes; else they are
+// gathered again.
+template <bool kOnce>
 __global__ void __launch_bounds__(kThreads) move_kernel(Move a) {
-  __shared__ int64_t src[KV8_MAX_PAGE];
-  __shared__ float scale[KV8_MAX_PAGE], red[kThreads / 64];
-  const int tid = threadIdx.x, P = 1 << a.c.lp, D = a.c.dim;
-  const bool value = blockIdx.x & 1;
-  const int place = blockIdx.x >> 1, h = place % a.c.heads, rest = place / a.c.heads, b = rest / a.blocks;
-  const Span p = span_of(a.s, b);
-  const int64_t asked = a.kept[b], kept = asked < 0 ? 0 : asked < a.keep ? asked : a.keep;
-  for (int64_t j = rest % a.blocks; j < a.to_blocks && (j << a.c.lp) < kept; j += a.blocks) {
-    const int to = a.to[b * a.to_stride + j];
-    if (to < 0 || to >= a.c.pages) continue;
-    const int n = static_cast<int>(kept - (j << a.c.lp) < P ? kept - (j << a.c.lp) : P);
-    const int64_t dest = static_cast<int64_t>(to) * a.c.heads + h;
-    __syncthreads();
-    if (tid < n) {
-      const int64_t t = a.index[(static_cast<int64_t>(b) * a.c.heads + h) * a.keep + (j << a.c.lp) + tid];
-      const int page = t >= 0 && t < p.len ? page_of(a.s, b, t >> a.c.lp, a.c.pages) : -1;
-      const int64_t at = static_cast<int64_t>(page) * a.c.heads + h, slot = t & (P - 1);
-      src[tid] = page < 0 ? -1 : (at << a.c.lp) * D + (value ? slot : slot * D);
-      scale[tid] = page < 0 ? 0.0f : (value ? a.c.v_scale : a.c.k_scale)[at];
-      if (!value && a.mass) a.mass[(dest << a.c.lp) + tid] = page < 0 ? 0.0f : a.mass[(at << a.c.lp) + slot];
+  __shared__ float red[kThreads / 64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (4 / a.waves) + wave / a.waves;
+  const int P = 1 << a.c.lp, D = a.c.dim, first = (wave % a.waves) * 64 + lane, threads = a.waves * 64;
+  const bool value = item & 1;
+  const int place = static_cast<int>(item >> 1), rest = a.c.by_heads.of(place), h = place - rest * a.c.heads;
+  const int b = a.by_blocks.of(rest), j = rest - b * a.blocks;
+  int n = 0, len = 0;
+  int64_t dest = 0;  // page and head
+  if (item < a.items) {
+    const int kept = a.kept[b] < a.keep ? a.kept[b] : a.keep, begin = j << a.c.lp, to = a.to[b * a.to_stride + j];
+    len = a.s.lens[b];
+    if (begin < kept && to >= 0 && to < a.c.pages) n = kept - begin < P ? kept - begin : P;
+    dest = static_cast<int64_t>(to) * a.c.heads + h;
+  }
+  const int32_t *index = a.index + (static_cast<int64_t>(b) * a.c.heads + h) * a.keep + (static_cast<int64_t>(j) << a.c.lp);
+  // Token i of the page: where it lies (page and head; -1: nowhere) and its slot.
+  auto find_token = [&](int i, int64_t &at, int &slot) {
+    const int t = index[i];
+    const int page = t >= 0 && t < len ? page_of(a.s, b, t >> a.c.lp, a.c.pages) : -1;
+    at = page < 0 ? -1 : static_cast<int64_t>(page) * a.c.heads + h;
+    slot = t & (P - 1);
+  };
+  float amax = 0.0f;
+
+  // Keys: units first, first + threads, ...
+  const int per = D / 16, units = n * per;
+  i32x4 key[kMoveUnits];
+  float key_scale[kMoveUnits];
+  auto load_keys = [&](int u0) {
+#pragma unroll
+    for (int k = 0; k < kMoveUnits; ++k) {
+      const int u = u0 + k * threads, i = a.by_units.of(u);
+      key[k] = i32x4{0, 0, 0, 0};
+      key_scale[k] = 0.0f;
+      if (u >= units) continue;
+      int64_t at;
+      int slot;
+      find_token(i, at, slot);
+      if (at < 0) continue;
+      key[k] = reinterpret_cast<const i32x4 *>(a.c.k)[((at << a.c.lp) + slot) * per + (u - i * per)];
+      key_scale[k] = a.c.k_scale[at];
     }
-    __syncthreads();
-    const int8_t *codes = value ? a.c.v : a.c.k;
-    int8_t *out = (value ? a.c.v : a.c.k) + (dest << a.c.lp) * D;
-    auto get = [&](int i, int d) { return src[i] < 0 ? 0.0f : static_cast<float>(codes[src[i] + (value ? d * P : d)]) * scale[i]; };
-    float amax = 0.0f;
-    for (int x = tid; x < P * D; x += kThreads) {
-      const int i = value ? x % P : x / D, d = value ? x / P : x % D;
-      if (i < n) amax = fmaxf(amax, fabsf(get(i, d)));
+  };
+  // Values: component group, group + step, ... of token `mine`.
+  const int mine = first & (P - 1), group = first >> a.c.lp, step = threads >> a.c.lp;
+  const int8_t *from = a.c.v;
+  float value_scale = 0.0f;
+  bool there = false;
+  int8_t byte[kMoveBytes];
+  auto load_values = [&](int d0) {
+#pragma unroll
+    for (int k = 0; k < kMoveBytes; ++k) {
+      const int d = d0 + k * step;
+      byte[k] = 0;
+      if (there && d < D) byte[k] = from[d << a.c.lp];
     }
-    amax = wave_max(amax);
-    if ((tid & 63) == 0) red[tid >> 6] = amax;
-    __syncthreads();
-    amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float s = fmaxf(amax, kAmaxFloor) / 127.0f;
-    if (tid == 0) (value ? a.c.v_scale : a.c.k_scale)[dest] = s;
-    for (int x = tid; x < P * D; x += kThreads) {
-      const int i = value ? x % P : x / D, d = value ? x / P : x % D;
-      if (i < n) out[x] = static_cast<int8_t>(code_of(get(i, d) / s));
+  };
+
+  if (!value) {
+    for (int u0 = first; u0 < units; u0 += kMoveUnits * threads) {
+      load_keys(u0);
+#pragma unroll
+      for (int k = 0; k < kMoveUnits; ++k) {
+        int most = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int code = static_cast<int8_t>(key[k][i / 4] >> (8 * (i % 4)));
+          most = most > code ? most : code;
+          most = most > -code ? most : -code;
+        }
+        amax = fmaxf(amax, static_cast<float>(most) * key_scale[k]);  // the largest product is the largest code's
+      }
+    }
+  } else if (mine < n) {
+    int64_t at;
+    int slot;
+    find_token(mine, at, slot);
+    there = at >= 0;
+    if (there) {
+      from = a.c.v + (at << a.c.lp) * D + slot;
+      value_scale = a.c.v_scale[at];
+    }
+    if (a.mass && group == 0) a.mass[(dest << a.c.lp) + mine] = there ? a.mass[(at << a.c.lp) + slot] : 0.0f;
+    int most = 0;
+    for (int d0 = group; d0 < D; d0 += kMoveBytes * step) {
+      load_values(d0);
+#pragma unroll
+      for (int k = 0; k < kMoveBytes; ++k) {
+        const int code = byte[k];
+        most = most > code ? most : code;
+        most = most > -code ? most : -code;
+      }
+    }
+    amax = static_cast<float>(most) * value_scale;
+  }
+  amax = wave_max(amax);
+  if (lane == 0) red[wave] = amax;
+  __syncthreads();
+  if (n == 0) return;
+  for (int k = 0; k < a.waves; ++k) amax = fmaxf(amax, red[wave / a.waves * a.waves + k]);
+  const float now = fmaxf(amax, kAmaxFloor) / 127.0f, inv = 1.0f / now;
+  if (first == 0) (value ? a.c.v_scale : a.c.k_scale)[dest] = now;
+  if (!value) {
+    i32x4 *out = reinterpret_cast<i32x4 *>(a.c.k) + (dest << a.c.lp) * per;
+    for (int u0 = first; u0 < units; u0 += kMoveUnits * threads) {
+      if (!kOnce) load_keys(u0);
+#pragma unroll
+      for (int k = 0; k < kMoveUnits; ++k) {
+        const int u = u0 + k * threads;
+        if (u >= units) continue;
+        i32x4 code;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          float x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = static_cast<float>(static_cast<int8_t>(key[k][w] >> (8 * i))) * key_scale[k];
+          code[w] = static_cast<int>(codes_of(x, now, inv));
+        }
+        out[u] = code;
+      }
+    }
+  } else if (mine < n) {
+    int8_t *out = a.c.v + (dest << a.c.lp) * D + mine;
+    for (int d0 = group; d0 < D; d0 += kMoveBytes * step) {
+      if (!kOnce) load_values(d0);
+#pragma unroll
+      for (int k = 0; k < kMoveBytes; k += 4) {
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = static_cast<float>(byte[k + i]) * value_scale;
+        const uint32_t code = codes_of(x, now, inv);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int d = d0 + (k + i) * step;
+          if (d < D) out[d << a.c.lp] = static_cast<int8_t>(code >> (8 * i));
+        }
+      }
     }
   }
 }
@@ -580,7 +798,7 @@ extern "C" int kv8_weigh(const kv8_cache *cache, const kv8_batch *batch, int typ
                    : a.c.dim < 128 ? launch_weigh<T, 2, false>(p, a, on)
                                    : launch_weigh<T, 4, false>(p, a, on);
     if (st || p.parts == 1) return st;
-    weigh_join_kernel<<<static_cast<unsigned>(p.each * p.blocks), kThreads, 0, on>>>(a);
+    weigh_join_kernel<<<static_cast<unsigned>(p.each * p.blocks * (kBlockTokens / kJoinTokens)), kThreads, 0, on>>>(a);
     return hip_status();
   });
 }
@@ -590,17 +808,21 @@ extern "C" int kv8_choose(const kv8_cache *cache, const kv8_batch *batch, const 
   Choose a;
   if (const int st = check_batch(cache, batch, KV8_F32, 0, a.c, a.s)) return st;
   if (keep < 0 || first < 0 || recent < 0 || first > keep || recent > keep - first) return I2S_EINVAL;
-  if (keep > kMaxRows - 1024 || (static_cast<int64_t>(a.s.blocks) << a.c.lp) > kMaxRows - 1024) return I2S_ERANGE;
+  if (keep > kMaxRows - 1024 || (static_cast<int64_t>(a.s.blocks) << a.c.lp) > kMaxRows - 65536) return I2S_ERANGE;
   if (a.s.seqs == 0) return I2S_OK;
   if (!mass || !aligned(mass, 4) || (keep > 0 && !index) || !aligned(index, 4) || !kept || !aligned(kept, 4)) return I2S_EINVAL;
   a.mass = mass;
-  a.keep = keep;
+  a.keep = static_cast<int>(keep);
   a.first = static_cast<int>(first);
   a.recent = static_cast<int>(recent);
   a.index = index;
   a.kept = kept;
-  choose_kernel<<<static_cast<unsigned>(a.s.seqs * a.c.heads), kChooseThreads, 0, static_cast<hipStream_t>(stream)>>>(a);
-  return hip_status();
+  const int64_t tokens = tokens_of(batch, a.c, a.s);
+  auto launch = [&](auto kernel) {
+    kernel<<<static_cast<unsigned>(a.s.seqs * a.c.heads), kChooseThreads, 0, static_cast<hipStream_t>(stream)>>>(a);
+    return hip_status();
+  };
+  return tokens <= 4 * 4096 ? launch(choose_kernel<4>) : launch(choose_kernel<16>);
 }
 
 extern "C" int kv8_move(const kv8_cache *cache, const kv8_batch *batch, const int32_t *index, const int32_t *kept, int64_t keep,
@@ -615,12 +837,27 @@ extern "C" int kv8_move(const kv8_cache *cache, const kv8_batch *batch, const in
   a.index = index;
   a.kept = kept;
   a.to = to_table;
-  a.keep = keep;
+  a.keep = static_cast<int>(keep);
   a.to_stride = to_stride;
   a.to_blocks = static_cast<int>(to_blocks);
   a.mass = mass;
-  const int64_t wanted = (keep + (INT64_C(1) << a.c.lp) - 1) >> a.c.lp, each = static_cast<int64_t>(a.s.seqs) * a.c.heads * 2;
-  a.blocks = pieces_of(wanted < to_blocks ? wanted : to_blocks, each);
-  move_kernel<<<static_cast<unsigned>(each * a.blocks), kThreads, 0, static_cast<hipStream_t>(stream)>>>(a);
+  const int64_t wanted = (keep + (INT64_C(1) << a.c.lp) - 1) >> a.c.lp, P = INT64_C(1) << a.c.lp;
+  a.blocks = static_cast<int>(wanted < to_blocks ? wanted : to_blocks);
+  a.by_blocks = Divisor(a.blocks);
+  a.by_units = Divisor(a.c.dim / 16);
+  const int64_t places = static_cast<int64_t>(a.s.seqs) * a.c.heads;
+  if (places > 0x7fffffff / a.blocks) return I2S_ERANGE;
+  a.items = 2 * places * a.blocks;
+  a.waves = P * a.c.dim <= 1024 ? 1 : P * a.c.dim <= 2048 ? 2 : 4;
+  const int64_t grid = (a.items * a.waves + 3) / 4;
+  if (grid > 0x7fffffff) return I2S_ERANGE;
+  auto launch = [&](auto kernel) {
+    kernel<<<static_cast<unsigned>(grid), kThreads, 0, static_cast<hipStream_t>(stream)>>>(a);
+  };
+  if (P * a.c.dim <= 16 * kMoveUnits * kThreads) {
+    launch(move_kernel<true>);
+  } else {
+    launch(move_kernel<false>);
+  }
   return hip_status();
 }
