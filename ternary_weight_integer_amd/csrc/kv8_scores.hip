@@ -529,42 +529,81 @@ struct Move {
 };
 
 constexpr int kMoveUnits = 2, kMoveBytes = 32;  // of a lane at a time
+constexpr int kMovePages = 4;                   // source pages that a wave looks at together
+constexpr int kTileBytes = 64 * kMoveBytes, kTilePad = 64;  // rows of 64 bytes in different pages: other banks
+
+// The largest and least of codes, in the high bytes of pairs of 16 bits (what is
+// below them does not reach up).
+struct Extremes {
+  typedef short S2 __attribute__((ext_vector_type(2)));
+  S2 high = {0, 0}, low = {0, 0};
+
+  __device__ void take(int codes) {
+    const S2 odd = __builtin_bit_cast(S2, codes), even = __builtin_bit_cast(S2, codes << 8);
+    high = __builtin_elementwise_max(high, __builtin_elementwise_max(odd, even));
+    low = __builtin_elementwise_min(low, __builtin_elementwise_min(odd, even));
+  }
+  __device__ float magnitude() const {
+    const int up = (high[0] > high[1] ? high[0] : high[1]) >> 8, down = -((low[0] < low[1] ? low[0] : low[1]) >> 8);
+    return static_cast<float>(up > down ? up : down);
+  }
+};
+
+// Byte i of the four lanes of a quad, in their order, to its lane i.
+__device__ inline uint32_t quad_turned(uint32_t code) {
+  const int c = static_cast<int>(code);
+  const uint32_t a = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(c, c, 0x00, 0xF, 0xF, false));  // lane 0's
+  const uint32_t b = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(c, c, 0x55, 0xF, 0xF, false));
+  const uint32_t d = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(c, c, 0xAA, 0xF, 0xF, false));
+  const uint32_t e = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(c, c, 0xFF, 0xF, 0xF, false));
+  const uint32_t i = threadIdx.x & 3, pair = i | (i + 4) << 8 | 0x0c0c0000u;
+  return __builtin_amdgcn_perm(b, a, pair) | __builtin_amdgcn_perm(e, d, pair) << 16;
+}
 
 // An item is a page to fill, a head, and K or V.  Keys are gathered 16 bytes a
-// lane; of V, tokens innermost, a lane has one token and takes its components
-// byte by byte: neighbouring lanes' tokens rise, so a wave's bytes of one
-// component lie in the few lines that these tokens span.  kOnce: the item's
-// codes stay in registers between the maximum and the new codes; else they are
-// gathered again.
-template <bool kOnce>
+// lane.  Of V, tokens innermost, a lane has one token and up to 32 of its
+// components, single bytes: a wave brings its components of the pages that its
+// tokens lie in, four at a time, to its own part of shared memory in whole
+// lines and picks them there.  (Picked from memory, 64 bytes were some 25
+// accesses of the cache: a batch of 40 took 272 us.)  Pages of over 64
+// tokens are picked from memory.  kOnce: the item's codes stay in registers
+// between the maximum and the new codes; else they are gathered again.
+template <bool kOnce, bool kStaged>
 __global__ void __launch_bounds__(kThreads) move_kernel(Move a) {
   __shared__ float red[kThreads / 64];
+  __shared__ i32x4 tiles[kStaged ? kThreads / 64 : 1][kStaged ? kMovePages : 1][(kTileBytes + kTilePad) / 16];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * (4 / a.waves) + wave / a.waves;
-  const int P = 1 << a.c.lp, D = a.c.dim, first = (wave % a.waves) * 64 + lane, threads = a.waves * 64;
+  const int P = 1 << a.c.lp, D = a.c.dim, part = wave % a.waves, first = part * 64 + lane, threads = a.waves * 64;
   const bool value = item & 1;
   const int place = static_cast<int>(item >> 1), rest = a.c.by_heads.of(place), h = place - rest * a.c.heads;
   const int b = a.by_blocks.of(rest), j = rest - b * a.blocks;
+  const int per = D / 16, begin = j << a.c.lp, left = a.keep - begin;
+  const int mine = first & (P - 1);  // of V: the lane's token
   int n = 0, len = 0;
   int64_t dest = 0;  // page and head
+  const int32_t *index = nullptr;
+  int chosen[kMoveUnits];  // tokens of the lane's units, or its own
   if (item < a.items) {
-    const int kept = a.kept[b] < a.keep ? a.kept[b] : a.keep, begin = j << a.c.lp, to = a.to[b * a.to_stride + j];
+    index = a.index + (static_cast<int64_t>(b) * a.c.heads + h) * a.keep + begin;
+    // Loads that wait for nothing, together.
+    const int asked = a.kept[b], to = a.to[b * a.to_stride + j];
     len = a.s.lens[b];
+#pragma unroll
+    for (int k = 0; k < kMoveUnits; ++k) {
+      const int i = value ? mine : a.by_units.of(first + k * threads);
+      chosen[k] = index[i < left ? i : left - 1];
+    }
+    const int kept = asked < a.keep ? asked : a.keep;
     if (begin < kept && to >= 0 && to < a.c.pages) n = kept - begin < P ? kept - begin : P;
     dest = static_cast<int64_t>(to) * a.c.heads + h;
   }
-  const int32_t *index = a.index + (static_cast<int64_t>(b) * a.c.heads + h) * a.keep + (static_cast<int64_t>(j) << a.c.lp);
-  // Token i of the page: where it lies (page and head; -1: nowhere) and its slot.
-  auto find_token = [&](int i, int64_t &at, int &slot) {
-    const int t = index[i];
-    const int page = t >= 0 && t < len ? page_of(a.s, b, t >> a.c.lp, a.c.pages) : -1;
-    at = page < 0 ? -1 : static_cast<int64_t>(page) * a.c.heads + h;
-    slot = t & (P - 1);
-  };
+  // The page that a token lies in, -1 for none.
+  auto page_of_token = [&](int t) { return t >= 0 && t < len ? page_of(a.s, b, t >> a.c.lp, a.c.pages) : -1; };
   float amax = 0.0f;
 
   // Keys: units first, first + threads, ...
-  const int per = D / 16, units = n * per;
+  const int units = n * per;
   i32x4 key[kMoveUnits];
   float key_scale[kMoveUnits];
   auto load_keys = [&](int u0) {
@@ -574,26 +613,84 @@ __global__ void __launch_bounds__(kThreads) move_kernel(Move a) {
       key[k] = i32x4{0, 0, 0, 0};
       key_scale[k] = 0.0f;
       if (u >= units) continue;
-      int64_t at;
-      int slot;
-      find_token(i, at, slot);
-      if (at < 0) continue;
-      key[k] = reinterpret_cast<const i32x4 *>(a.c.k)[((at << a.c.lp) + slot) * per + (u - i * per)];
+      const int t = u0 == first ? chosen[k] : index[i], page = page_of_token(t);
+      if (page < 0) continue;
+      const int64_t at = static_cast<int64_t>(page) * a.c.heads + h;
+      key[k] = reinterpret_cast<const i32x4 *>(a.c.k)[((at << a.c.lp) + (t & (P - 1))) * per + (u - i * per)];
       key_scale[k] = a.c.k_scale[at];
     }
   };
-  // Values: component group, group + step, ... of token `mine`.
-  const int mine = first & (P - 1), group = first >> a.c.lp, step = threads >> a.c.lp;
-  const int8_t *from = a.c.v;
+
+  // Values: components start, start + step, ... below end of token `mine`, 32 a
+  // round.  Staged: a wave has a share of the components of all tokens.
+  const int share = D / a.waves;
+  const int start = kStaged ? part * share + (lane >> a.c.lp) : first >> a.c.lp, end = kStaged ? (part + 1) * share : D;
+  const int step = (kStaged ? 64 : threads) >> a.c.lp;
+  int from = -1;  // page
   float value_scale = 0.0f;
-  bool there = false;
-  int8_t byte[kMoveBytes];
+  int packed[kMoveBytes / 4];
   auto load_values = [&](int d0) {
+    if constexpr (kStaged) {
 #pragma unroll
-    for (int k = 0; k < kMoveBytes; ++k) {
-      const int d = d0 + k * step;
-      byte[k] = 0;
-      if (there && d < D) byte[k] = from[d << a.c.lp];
+      for (int k = 0; k < kMoveBytes / 4; ++k) packed[k] = 0;
+      // The wave's rows of a page: components row0 .. row0 + rows - 1.
+      const int row0 = __builtin_amdgcn_readfirstlane(d0), rows = end - row0 < kMoveBytes * step ? end - row0 : kMoveBytes * step;
+      const int bytes = rows << a.c.lp;
+      uint64_t pending = __ballot(from >= 0);
+      while (pending) {
+        i32x4 tile[kMovePages][2];
+        int held = -1;
+#pragma unroll
+        for (int k = 0; k < kMovePages; ++k) {
+          const int page = __builtin_amdgcn_readlane(from, pending ? __builtin_ctzll(pending) : 0);
+          const uint64_t same = pending & __ballot(from == page);
+          if ((same >> lane) & 1) held = k;
+          const int8_t *src = a.c.v + (((static_cast<int64_t>(page < 0 ? 0 : page) * a.c.heads + h) * D + row0) << a.c.lp);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) tile[k][u] = i32x4{0, 0, 0, 0};
+          if (pending) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              if (16 * (lane + 64 * u) < bytes) tile[k][u] = reinterpret_cast<const i32x4 *>(src)[lane + 64 * u];
+          }
+          pending &= ~same;
+        }
+#pragma unroll
+        for (int k = 0; k < kMovePages; ++k) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) tiles[wave][k][lane + 64 * u] = tile[k][u];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        if (held >= 0) {
+          const uint8_t *src = reinterpret_cast<const uint8_t *>(tiles[wave][held]) + ((lane >> a.c.lp) << a.c.lp) + (chosen[0] & (P - 1));
+#pragma unroll
+          for (int k = 0; k < kMoveBytes; k += 4) {
+            uint8_t byte[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) byte[i] = src[64 * (k + i)];  // step components further on: 64 bytes
+            packed[k / 4] = static_cast<int>(pack_bytes(byte[0], byte[1], byte[2], byte[3]));
+          }
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+    } else {
+      const int8_t *p = a.c.v + (((static_cast<int64_t>(from < 0 ? 0 : from) * a.c.heads + h) * D + d0) << a.c.lp) + (chosen[0] & (P - 1));
+#pragma unroll
+      for (int k = 0; k < kMoveBytes; k += 16) {
+        int8_t byte[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          byte[i] = 0;
+          if (d0 + (k + i) * step < D) byte[i] = *p;
+          p += step << a.c.lp;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          packed[(k + i) / 4] = static_cast<int>(pack_bytes(static_cast<uint8_t>(byte[i]), static_cast<uint8_t>(byte[i + 1]),
+                                                            static_cast<uint8_t>(byte[i + 2]), static_cast<uint8_t>(byte[i + 3])));
+      }
     }
   };
 
@@ -602,37 +699,27 @@ __global__ void __launch_bounds__(kThreads) move_kernel(Move a) {
       load_keys(u0);
 #pragma unroll
       for (int k = 0; k < kMoveUnits; ++k) {
-        int most = 0;
+        Extremes x;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int code = static_cast<int8_t>(key[k][i / 4] >> (8 * (i % 4)));
-          most = most > code ? most : code;
-          most = most > -code ? most : -code;
-        }
-        amax = fmaxf(amax, static_cast<float>(most) * key_scale[k]);  // the largest product is the largest code's
+        for (int i = 0; i < 4; ++i) x.take(key[k][i]);
+        amax = fmaxf(amax, x.magnitude() * key_scale[k]);  // the largest product is the largest code's
       }
+      if (kOnce) break;
     }
-  } else if (mine < n) {
-    int64_t at;
-    int slot;
-    find_token(mine, at, slot);
-    there = at >= 0;
-    if (there) {
-      from = a.c.v + (at << a.c.lp) * D + slot;
-      value_scale = a.c.v_scale[at];
-    }
-    if (a.mass && group == 0) a.mass[(dest << a.c.lp) + mine] = there ? a.mass[(at << a.c.lp) + slot] : 0.0f;
-    int most = 0;
-    for (int d0 = group; d0 < D; d0 += kMoveBytes * step) {
+  } else if (n > 0) {
+    from = mine < n ? page_of_token(chosen[0]) : -1;
+    if (from >= 0) value_scale = a.c.v_scale[static_cast<int64_t>(from) * a.c.heads + h];
+    if (a.mass && start == 0 && mine < n)
+      a.mass[(dest << a.c.lp) + mine] =
+          from < 0 ? 0.0f : a.mass[((static_cast<int64_t>(from) * a.c.heads + h) << a.c.lp) + (chosen[0] & (P - 1))];
+    Extremes x;
+    for (int d0 = start; kStaged ? __builtin_amdgcn_readfirstlane(d0) < end : d0 < end; d0 += kMoveBytes * step) {
       load_values(d0);
 #pragma unroll
-      for (int k = 0; k < kMoveBytes; ++k) {
-        const int code = byte[k];
-        most = most > code ? most : code;
-        most = most > -code ? most : -code;
-      }
+      for (int k = 0; k < kMoveBytes / 4; ++k) x.take(packed[k]);
+      if (kOnce) break;
     }
-    amax = static_cast<float>(most) * value_scale;
+    amax = x.magnitude() * value_scale;
   }
   amax = wave_max(amax);
   if (lane == 0) red[wave] = amax;
@@ -641,6 +728,16 @@ __global__ void __launch_bounds__(kThreads) move_kernel(Move a) {
   for (int k = 0; k < a.waves; ++k) amax = fmaxf(amax, red[wave / a.waves * a.waves + k]);
   const float now = fmaxf(amax, kAmaxFloor) / 127.0f, inv = 1.0f / now;
   if (first == 0) (value ? a.c.v_scale : a.c.k_scale)[dest] = now;
+  // The codes alone are kept until here, not what was made of them: a third of
+  // the registers.
+  if (kOnce && !value) {
+#pragma unroll
+    for (int k = 0; k < kMoveUnits; ++k) asm volatile("" : "+v"(key[k]));
+  }
+  if (kOnce && value) {
+#pragma unroll
+    for (int k = 0; k < kMoveBytes / 4; ++k) asm volatile("" : "+v"(packed[k]));
+  }
   if (!value) {
     i32x4 *out = reinterpret_cast<i32x4 *>(a.c.k) + (dest << a.c.lp) * per;
     for (int u0 = first; u0 < units; u0 += kMoveUnits * threads) {
@@ -659,23 +756,34 @@ __global__ void __launch_bounds__(kThreads) move_kernel(Move a) {
         }
         out[u] = code;
       }
+      if (kOnce) break;
     }
-  } else if (mine < n) {
-    int8_t *out = a.c.v + (dest << a.c.lp) * D + mine;
-    for (int d0 = group; d0 < D; d0 += kMoveBytes * step) {
+  } else {
+    for (int d0 = start; kStaged ? __builtin_amdgcn_readfirstlane(d0) < end : d0 < end; d0 += kMoveBytes * step) {
       if (!kOnce) load_values(d0);
+      int8_t *out = a.c.v + ((dest * D + d0) << a.c.lp) + mine;
+      // Four lanes turn their 4 x 4 bytes: each then has four tokens of one
+      // component, and stores four bytes where all four tokens are new ones.
+      const bool whole = (mine | 3) < n;
+      int8_t *out4 = out - (lane & 3) + static_cast<int64_t>(lane & 3) * (step << a.c.lp);
 #pragma unroll
       for (int k = 0; k < kMoveBytes; k += 4) {
         float x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = static_cast<float>(byte[k + i]) * value_scale;
+        for (int i = 0; i < 4; ++i) x[i] = static_cast<float>(static_cast<int8_t>(packed[k / 4] >> (8 * i))) * value_scale;
         const uint32_t code = codes_of(x, now, inv);
+        const uint32_t turned = quad_turned(code);
+        if (whole) {
+          if (d0 + (k + (lane & 3)) * step < end) *reinterpret_cast<uint32_t *>(out4) = turned;
+        } else if (mine < n) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int d = d0 + (k + i) * step;
-          if (d < D) out[d << a.c.lp] = static_cast<int8_t>(code >> (8 * i));
+          for (int i = 0; i < 4; ++i)
+            if (d0 + (k + i) * step < end) out[i * (step << a.c.lp)] = static_cast<int8_t>(code >> (8 * i));
         }
+        out += 4 * (step << a.c.lp);
+        out4 += 4 * (step << a.c.lp);
       }
+      if (kOnce) break;
     }
   }
 }
@@ -854,10 +962,11 @@ extern "C" int kv8_move(const kv8_cache *cache, const kv8_batch *batch, const in
   auto launch = [&](auto kernel) {
     kernel<<<static_cast<unsigned>(grid), kThreads, 0, static_cast<hipStream_t>(stream)>>>(a);
   };
-  if (P * a.c.dim <= 16 * kMoveUnits * kThreads) {
-    launch(move_kernel<true>);
+  const bool once = P * a.c.dim <= 16 * kMoveUnits * kThreads;
+  if (P <= 64) {
+    launch(once ? move_kernel<true, true> : move_kernel<false, true>);
   } else {
-    launch(move_kernel<false>);
+    launch(once ? move_kernel<true, false> : move_kernel<false, false>);
   }
   return hip_status();
 }
