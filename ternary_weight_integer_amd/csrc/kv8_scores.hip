@@ -529,7 +529,7 @@ struct Move {
 };
 
 constexpr int kMoveUnits = 2, kMoveBytes = 32;  // of a lane at a time
-constexpr int kMovePages = 4;                   // source pages that a wave looks at together
+constexpr int kMovePages = 2;                   // source pages that a wave looks at together
 constexpr int kTileBytes = 64 * kMoveBytes, kTilePad = 64;  // rows of 64 bytes in different pages: other banks
 
 // The largest and least of codes, in the high bytes of pairs of 16 bits (what is
@@ -549,6 +549,28 @@ struct Extremes {
   }
 };
 
+// Four codes of scale s as codes of scale now: round_half_away((c s) / now),
+// |c s| <= 127 now.  With ratio = s (1 / now) c ratio and that quotient, each
+// rounded twice, lie within 4 127 2^-24 = 3.1e-5 of each other, so where c ratio
+// is 2^-14 and more off the middle of two integers both round to the same: one
+// fused product and sum (1.5 * 2^23 leaves the integer lowest), and a second for
+// what is left of it.
+__device__ inline uint32_t recoded(int codes, float ratio, float s, float now) {
+  float r[4], most = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float c = static_cast<float>(static_cast<int8_t>(codes >> (8 * j)));
+    r[j] = fmaf(c, ratio, 0x1.8p23f);
+    most = fmaxf(most, fabsf(fmaf(c, ratio, 0x1.8p23f - r[j])));
+  }
+  if (most > 0.5f - 0x1p-14f) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      r[j] = static_cast<float>(code_of(static_cast<float>(static_cast<int8_t>(codes >> (8 * j))) * s / now)) + 0x1.8p23f;
+  }
+  return pack_bytes(__float_as_uint(r[0]), __float_as_uint(r[1]), __float_as_uint(r[2]), __float_as_uint(r[3]));
+}
+
 // Byte i of the four lanes of a quad, in their order, to its lane i.
 __device__ inline uint32_t quad_turned(uint32_t code) {
   const int c = static_cast<int>(code);
@@ -560,49 +582,47 @@ __device__ inline uint32_t quad_turned(uint32_t code) {
   return __builtin_amdgcn_perm(b, a, pair) | __builtin_amdgcn_perm(e, d, pair) << 16;
 }
 
-// An item is a page to fill, a head, and K or V.  Keys are gathered 16 bytes a
-// lane.  Of V, tokens innermost, a lane has one token and up to 32 of its
-// components, single bytes: a wave brings its components of the pages that its
-// tokens lie in, four at a time, to its own part of shared memory in whole
-// lines and picks them there.  (Picked from memory, 64 bytes were some 25
-// accesses of the cache: a batch of 40 took 272 us.)  Pages of over 64
-// tokens are picked from memory.  kOnce: the item's codes stay in registers
-// between the maximum and the new codes; else they are gathered again.
+// An item is a page to fill and a head, its keys and values at once: what it
+// takes is the chain of count, index, page, codes, maximum and stores, and the
+// more of it is on its way at a time the better (keys and values apart: a batch
+// of 40 in 132 us, together 115).  Keys are gathered 16 bytes a lane.  Of V,
+// tokens innermost, a lane has one token and up to 32 of its components, single
+// bytes: a wave brings its components of the pages that its tokens lie in, two
+// at a time, to its own part of shared memory in whole lines and picks them there
+// (picked from memory, 64 bytes were some 25 accesses of the cache: 272 us).
+// Pages of over 64 tokens are picked from memory.  kOnce: the item's codes stay
+// in registers between the maximum and the new codes; else they are gathered
+// again.
 template <bool kOnce, bool kStaged>
 __global__ void __launch_bounds__(kThreads) move_kernel(Move a) {
-  __shared__ float red[kThreads / 64];
+  __shared__ float red[2][kThreads / 64];
   __shared__ i32x4 tiles[kStaged ? kThreads / 64 : 1][kStaged ? kMovePages : 1][(kTileBytes + kTilePad) / 16];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * (4 / a.waves) + wave / a.waves;
   const int P = 1 << a.c.lp, D = a.c.dim, part = wave % a.waves, first = part * 64 + lane, threads = a.waves * 64;
-  const bool value = item & 1;
-  const int place = static_cast<int>(item >> 1), rest = a.c.by_heads.of(place), h = place - rest * a.c.heads;
+  const int rest = a.c.by_heads.of(static_cast<int>(item)), h = static_cast<int>(item) - rest * a.c.heads;
   const int b = a.by_blocks.of(rest), j = rest - b * a.blocks;
   const int per = D / 16, begin = j << a.c.lp, left = a.keep - begin;
-  const int mine = first & (P - 1);  // of V: the lane's token
-  int n = 0, len = 0;
+  const int mine = first & (P - 1);  // the lane's token
+  int n = 0, len = 0, chosen = -1;
   int64_t dest = 0;  // page and head
   const int32_t *index = nullptr;
-  int chosen[kMoveUnits];  // tokens of the lane's units, or its own
   if (item < a.items) {
     index = a.index + (static_cast<int64_t>(b) * a.c.heads + h) * a.keep + begin;
     // Loads that wait for nothing, together.
     const int asked = a.kept[b], to = a.to[b * a.to_stride + j];
     len = a.s.lens[b];
-#pragma unroll
-    for (int k = 0; k < kMoveUnits; ++k) {
-      const int i = value ? mine : a.by_units.of(first + k * threads);
-      chosen[k] = index[i < left ? i : left - 1];
-    }
+    chosen = index[mine < left ? mine : left - 1];
     const int kept = asked < a.keep ? asked : a.keep;
     if (begin < kept && to >= 0 && to < a.c.pages) n = kept - begin < P ? kept - begin : P;
     dest = static_cast<int64_t>(to) * a.c.heads + h;
   }
-  // The page that a token lies in, -1 for none.
+  // The page that a token lies in, -1 for none, and that page's place for the head.
   auto page_of_token = [&](int t) { return t >= 0 && t < len ? page_of(a.s, b, t >> a.c.lp, a.c.pages) : -1; };
-  float amax = 0.0f;
+  auto at_page = [&](int page) { return static_cast<int64_t>(page) * a.c.heads + h; };
+  const int from = mine < n ? page_of_token(chosen) : -1, slot = chosen & (P - 1);
 
-  // Keys: units first, first + threads, ...
+  // Keys: units first, first + threads, ... of 16 bytes.
   const int units = n * per;
   i32x4 key[kMoveUnits];
   float key_scale[kMoveUnits];
@@ -610,14 +630,20 @@ __global__ void __launch_bounds__(kThreads) move_kernel(Move a) {
 #pragma unroll
     for (int k = 0; k < kMoveUnits; ++k) {
       const int u = u0 + k * threads, i = a.by_units.of(u);
+      int page, s;
+      if constexpr (kStaged) {  // lane i has token i
+        page = __shfl(from, i & 63);
+        s = __shfl(slot, i & 63);
+      } else {
+        const int t = u < units ? index[i] : -1;
+        page = page_of_token(t);
+        s = t & (P - 1);
+      }
       key[k] = i32x4{0, 0, 0, 0};
       key_scale[k] = 0.0f;
-      if (u >= units) continue;
-      const int t = u0 == first ? chosen[k] : index[i], page = page_of_token(t);
-      if (page < 0) continue;
-      const int64_t at = static_cast<int64_t>(page) * a.c.heads + h;
-      key[k] = reinterpret_cast<const i32x4 *>(a.c.k)[((at << a.c.lp) + (t & (P - 1))) * per + (u - i * per)];
-      key_scale[k] = a.c.k_scale[at];
+      if (u >= units || page < 0) continue;
+      key[k] = reinterpret_cast<const i32x4 *>(a.c.k)[((at_page(page) << a.c.lp) + s) * per + (u - i * per)];
+      key_scale[k] = a.c.k_scale[at_page(page)];
     }
   };
 
@@ -626,8 +652,7 @@ __global__ void __launch_bounds__(kThreads) move_kernel(Move a) {
   const int share = D / a.waves;
   const int start = kStaged ? part * share + (lane >> a.c.lp) : first >> a.c.lp, end = kStaged ? (part + 1) * share : D;
   const int step = (kStaged ? 64 : threads) >> a.c.lp;
-  int from = -1;  // page
-  float value_scale = 0.0f;
+  const float value_scale = from < 0 ? 0.0f : a.c.v_scale[at_page(from)];
   int packed[kMoveBytes / 4];
   auto load_values = [&](int d0) {
     if constexpr (kStaged) {
@@ -645,13 +670,11 @@ __global__ void __launch_bounds__(kThreads) move_kernel(Move a) {
           const int page = __builtin_amdgcn_readlane(from, pending ? __builtin_ctzll(pending) : 0);
           const uint64_t same = pending & __ballot(from == page);
           if ((same >> lane) & 1) held = k;
-          const int8_t *src = a.c.v + (((static_cast<int64_t>(page < 0 ? 0 : page) * a.c.heads + h) * D + row0) << a.c.lp);
+          const i32x4 *src = reinterpret_cast<const i32x4 *>(a.c.v + ((at_page(page < 0 ? 0 : page) * D + row0) << a.c.lp));
 #pragma unroll
-          for (int u = 0; u < 2; ++u) tile[k][u] = i32x4{0, 0, 0, 0};
-          if (pending) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              if (16 * (lane + 64 * u) < bytes) tile[k][u] = reinterpret_cast<const i32x4 *>(src)[lane + 64 * u];
+          for (int u = 0; u < 2; ++u) {
+            tile[k][u] = i32x4{0, 0, 0, 0};
+            if (pending && 16 * (lane + 64 * u) < bytes) tile[k][u] = src[lane + 64 * u];
           }
           pending &= ~same;
         }
@@ -664,7 +687,7 @@ __global__ void __launch_bounds__(kThreads) move_kernel(Move a) {
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         if (held >= 0) {
-          const uint8_t *src = reinterpret_cast<const uint8_t *>(tiles[wave][held]) + ((lane >> a.c.lp) << a.c.lp) + (chosen[0] & (P - 1));
+          const uint8_t *src = reinterpret_cast<const uint8_t *>(tiles[wave][held]) + ((lane >> a.c.lp) << a.c.lp) + slot;
 #pragma unroll
           for (int k = 0; k < kMoveBytes; k += 4) {
             uint8_t byte[4];
@@ -676,27 +699,31 @@ __global__ void __launch_bounds__(kThreads) move_kernel(Move a) {
         __builtin_amdgcn_wave_barrier();
       }
     } else {
-      const int8_t *p = a.c.v + (((static_cast<int64_t>(from < 0 ? 0 : from) * a.c.heads + h) * D + d0) << a.c.lp) + (chosen[0] & (P - 1));
+      const int8_t *p = a.c.v + ((at_page(from < 0 ? 0 : from) * D + d0) << a.c.lp) + slot;
 #pragma unroll
       for (int k = 0; k < kMoveBytes; k += 16) {
-        int8_t byte[16];
+        uint8_t byte[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           byte[i] = 0;
-          if (d0 + (k + i) * step < D) byte[i] = *p;
+          if (d0 + (k + i) * step < D) byte[i] = static_cast<uint8_t>(*p);
           p += step << a.c.lp;
         }
 #pragma unroll
         for (int i = 0; i < 16; i += 4)
-          packed[(k + i) / 4] = static_cast<int>(pack_bytes(static_cast<uint8_t>(byte[i]), static_cast<uint8_t>(byte[i + 1]),
-                                                            static_cast<uint8_t>(byte[i + 2]), static_cast<uint8_t>(byte[i + 3])));
+          packed[(k + i) / 4] = static_cast<int>(pack_bytes(byte[i], byte[i + 1], byte[i + 2], byte[i + 3]));
       }
     }
   };
 
-  if (!value) {
-    for (int u0 = first; u0 < units; u0 += kMoveUnits * threads) {
-      load_keys(u0);
+  float amax = 0.0f;
+  Extremes values;
+  if (n > 0) {
+    if (a.mass && start == 0 && mine < n)
+      a.mass[(dest << a.c.lp) + mine] = from < 0 ? 0.0f : a.mass[(at_page(from) << a.c.lp) + slot];
+    for (int u0 = part * 64; u0 < units; u0 += kMoveUnits * threads) {
+      load_keys(u0 + lane);
+      if (kOnce) break;
 #pragma unroll
       for (int k = 0; k < kMoveUnits; ++k) {
         Extremes x;
@@ -704,87 +731,85 @@ __global__ void __launch_bounds__(kThreads) move_kernel(Move a) {
         for (int i = 0; i < 4; ++i) x.take(key[k][i]);
         amax = fmaxf(amax, x.magnitude() * key_scale[k]);  // the largest product is the largest code's
       }
-      if (kOnce) break;
     }
-  } else if (n > 0) {
-    from = mine < n ? page_of_token(chosen[0]) : -1;
-    if (from >= 0) value_scale = a.c.v_scale[static_cast<int64_t>(from) * a.c.heads + h];
-    if (a.mass && start == 0 && mine < n)
-      a.mass[(dest << a.c.lp) + mine] =
-          from < 0 ? 0.0f : a.mass[((static_cast<int64_t>(from) * a.c.heads + h) << a.c.lp) + (chosen[0] & (P - 1))];
-    Extremes x;
     for (int d0 = start; kStaged ? __builtin_amdgcn_readfirstlane(d0) < end : d0 < end; d0 += kMoveBytes * step) {
       load_values(d0);
 #pragma unroll
-      for (int k = 0; k < kMoveBytes / 4; ++k) x.take(packed[k]);
+      for (int k = 0; k < kMoveBytes / 4; ++k) values.take(packed[k]);
       if (kOnce) break;
     }
-    amax = x.magnitude() * value_scale;
+    if (kOnce && part * 64 < units) {
+#pragma unroll
+      for (int k = 0; k < kMoveUnits; ++k) {
+        Extremes x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x.take(key[k][i]);
+        amax = fmaxf(amax, x.magnitude() * key_scale[k]);
+      }
+    }
   }
   amax = wave_max(amax);
-  if (lane == 0) red[wave] = amax;
+  float vmax = wave_max(values.magnitude() * value_scale);
+  if (lane == 0) {
+    red[0][wave] = amax;
+    red[1][wave] = vmax;
+  }
   __syncthreads();
   if (n == 0) return;
-  for (int k = 0; k < a.waves; ++k) amax = fmaxf(amax, red[wave / a.waves * a.waves + k]);
-  const float now = fmaxf(amax, kAmaxFloor) / 127.0f, inv = 1.0f / now;
-  if (first == 0) (value ? a.c.v_scale : a.c.k_scale)[dest] = now;
-  // The codes alone are kept until here, not what was made of them: a third of
-  // the registers.
-  if (kOnce && !value) {
+  for (int k = 0; k < a.waves; ++k) {
+    amax = fmaxf(amax, red[0][wave / a.waves * a.waves + k]);
+    vmax = fmaxf(vmax, red[1][wave / a.waves * a.waves + k]);
+  }
+  const float know = fmaxf(amax, kAmaxFloor) / 127.0f, kinv = 1.0f / know;
+  const float vnow = fmaxf(vmax, kAmaxFloor) / 127.0f, vinv = 1.0f / vnow;
+  if (first == 0) {
+    a.c.k_scale[dest] = know;
+    a.c.v_scale[dest] = vnow;
+  }
+  if (kOnce) {
+    // The codes alone are kept until here, not what was made of them: a third of
+    // the registers.
 #pragma unroll
     for (int k = 0; k < kMoveUnits; ++k) asm volatile("" : "+v"(key[k]));
-  }
-  if (kOnce && value) {
 #pragma unroll
     for (int k = 0; k < kMoveBytes / 4; ++k) asm volatile("" : "+v"(packed[k]));
   }
-  if (!value) {
-    i32x4 *out = reinterpret_cast<i32x4 *>(a.c.k) + (dest << a.c.lp) * per;
-    for (int u0 = first; u0 < units; u0 += kMoveUnits * threads) {
-      if (!kOnce) load_keys(u0);
+  i32x4 *keys = reinterpret_cast<i32x4 *>(a.c.k) + (dest << a.c.lp) * per;
+  for (int u0 = part * 64; u0 < units; u0 += kMoveUnits * threads) {
+    if (!kOnce) load_keys(u0 + lane);
 #pragma unroll
-      for (int k = 0; k < kMoveUnits; ++k) {
-        const int u = u0 + k * threads;
-        if (u >= units) continue;
-        i32x4 code;
+    for (int k = 0; k < kMoveUnits; ++k) {
+      const int u = u0 + lane + k * threads;
+      if (u >= units) continue;
+      i32x4 code;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          float x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = static_cast<float>(static_cast<int8_t>(key[k][w] >> (8 * i))) * key_scale[k];
-          code[w] = static_cast<int>(codes_of(x, now, inv));
-        }
-        out[u] = code;
-      }
-      if (kOnce) break;
+      for (int w = 0; w < 4; ++w) code[w] = static_cast<int>(recoded(key[k][w], key_scale[k] * kinv, key_scale[k], know));
+      keys[u] = code;
     }
-  } else {
-    for (int d0 = start; kStaged ? __builtin_amdgcn_readfirstlane(d0) < end : d0 < end; d0 += kMoveBytes * step) {
-      if (!kOnce) load_values(d0);
-      int8_t *out = a.c.v + ((dest * D + d0) << a.c.lp) + mine;
-      // Four lanes turn their 4 x 4 bytes: each then has four tokens of one
-      // component, and stores four bytes where all four tokens are new ones.
-      const bool whole = (mine | 3) < n;
-      int8_t *out4 = out - (lane & 3) + static_cast<int64_t>(lane & 3) * (step << a.c.lp);
+    if (kOnce) break;
+  }
+  // Four lanes turn their 4 x 4 bytes: each then has four tokens of one
+  // component, and stores four bytes where all four tokens are new ones.
+  const bool whole = (mine | 3) < n;
+  for (int d0 = start; kStaged ? __builtin_amdgcn_readfirstlane(d0) < end : d0 < end; d0 += kMoveBytes * step) {
+    if (!kOnce) load_values(d0);
+    int8_t *out = a.c.v + ((dest * D + d0) << a.c.lp) + mine;
+    int8_t *out4 = out - (lane & 3) + static_cast<int64_t>(lane & 3) * (step << a.c.lp);
 #pragma unroll
-      for (int k = 0; k < kMoveBytes; k += 4) {
-        float x[4];
+    for (int k = 0; k < kMoveBytes; k += 4) {
+      const uint32_t code = recoded(packed[k / 4], value_scale * vinv, value_scale, vnow);
+      const uint32_t turned = quad_turned(code);
+      if (whole) {
+        if (d0 + (k + (lane & 3)) * step < end) *reinterpret_cast<uint32_t *>(out4) = turned;
+      } else if (mine < n) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = static_cast<float>(static_cast<int8_t>(packed[k / 4] >> (8 * i))) * value_scale;
-        const uint32_t code = codes_of(x, now, inv);
-        const uint32_t turned = quad_turned(code);
-        if (whole) {
-          if (d0 + (k + (lane & 3)) * step < end) *reinterpret_cast<uint32_t *>(out4) = turned;
-        } else if (mine < n) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (d0 + (k + i) * step < end) out[i * (step << a.c.lp)] = static_cast<int8_t>(code >> (8 * i));
-        }
-        out += 4 * (step << a.c.lp);
-        out4 += 4 * (step << a.c.lp);
+        for (int i = 0; i < 4; ++i)
+          if (d0 + (k + i) * step < end) out[i * (step << a.c.lp)] = static_cast<int8_t>(code >> (8 * i));
       }
-      if (kOnce) break;
+      out += 4 * (step << a.c.lp);
+      out4 += 4 * (step << a.c.lp);
     }
+    if (kOnce) break;
   }
 }
 
@@ -955,7 +980,7 @@ extern "C" int kv8_move(const kv8_cache *cache, const kv8_batch *batch, const in
   a.by_units = Divisor(a.c.dim / 16);
   const int64_t places = static_cast<int64_t>(a.s.seqs) * a.c.heads;
   if (places > 0x7fffffff / a.blocks) return I2S_ERANGE;
-  a.items = 2 * places * a.blocks;
+  a.items = places * a.blocks;
   a.waves = P * a.c.dim <= 1024 ? 1 : P * a.c.dim <= 2048 ? 2 : 4;
   const int64_t grid = (a.items * a.waves + 3) / 4;
   if (grid > 0x7fffffff) return I2S_ERANGE;
