@@ -345,23 +345,24 @@ struct Choose {
   int32_t *index, *kept;
 };
 
-// A number that rises with the mass: 0 for a token that is none, 1 for a NaN,
-// the largest for one that always stays.
-__device__ inline uint32_t rank_of(float mass, bool always) {
-  if (always) return 0xffffffffu;
-  if (mass != mass) return 1;
+// A number that rises with the mass, 1 for a NaN.  0 is left for a token that
+// is none, the largest for one that always stays.
+__device__ inline uint32_t rank_of(float mass) {
   const uint32_t u = __float_as_uint(mass + 0.0f);  // -0 is 0
-  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  return mass != mass ? 1 : u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
+
+template <int kCtrl, int kRows>
+__device__ inline int dpp_or_zero(int v) { return __builtin_amdgcn_update_dpp(0, v, kCtrl, kRows, 0xF, false); }
 
 // Sum over the wave's lanes up to this one.
 __device__ inline int wave_scan(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int k = 1; k < 64; k *= 2) {
-    const int other = __shfl_up(v, k);
-    v += lane >= k ? other : 0;
-  }
+  v += dpp_or_zero<0x111, 0xF>(v);  // row_shr:1
+  v += dpp_or_zero<0x112, 0xF>(v);
+  v += dpp_or_zero<0x114, 0xF>(v);
+  v += dpp_or_zero<0x118, 0xF>(v);
+  v += dpp_or_zero<0x142, 0xA>(v);  // row_bcast:15, to rows 1 and 3
+  v += dpp_or_zero<0x143, 0xC>(v);  // row_bcast:31, to rows 2 and 3
   return v;
 }
 
@@ -370,11 +371,17 @@ __device__ inline int wave_scan(int v) {
 // walked in segments, each pass again.  The least rank that stays is found in
 // digits of 11, 11 and 10 bits from the highest, with a histogram of the ranks
 // that begin with the digits found; then the tokens are written in order.
+// A bin is four counters, of lanes 0, 4, ..; 1, 5, .. and so on: masses share
+// few exponents, and lanes that add to one counter take turns.
+// A sequence is one compute unit's work, bound by its vector instructions: ranks,
+// histograms and places.
 template <int kLoads>
 __global__ void __launch_bounds__(kChooseThreads) choose_kernel(Choose a) {
   constexpr int kSegment = kLoads * kChooseThreads * 4;
   typedef float F4 __attribute__((ext_vector_type(4), aligned(4)));
-  __shared__ int hist[kBins], waves[kChooseWaves], pick[2];
+  typedef int I4 __attribute__((ext_vector_type(4)));
+  __shared__ I4 hist[kBins];
+  __shared__ int waves[kChooseWaves], pick[2];
   __shared__ int base[2][kLoads * kChooseWaves];
   const int b = a.c.by_heads.of(blockIdx.x), h = blockIdx.x - b * a.c.heads;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -402,22 +409,27 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(Choose a) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const bool hole = static_cast<unsigned>(entry[i]) >= static_cast<unsigned>(a.c.pages);
+      const int64_t t = begin + static_cast<int64_t>(i) * (4 * kChooseThreads);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int64_t t = begin + static_cast<int64_t>(i) * (4 * kChooseThreads) + k;
-        rank[i][k] = hole || t >= top ? 0 : rank_of(m[i][k], t < a.first || t >= newest);
+      for (int k = 0; k < 4; ++k) rank[i][k] = rank_of(m[i][k]);
+      if (__any(hole || t < a.first || t + 3 >= newest || t + 3 >= top)) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          rank[i][k] = t + k < a.first || t + k >= newest ? 0xffffffffu : rank[i][k];
+          rank[i][k] = hole || t + k >= top ? 0 : rank[i][k];
+        }
       }
     }
   };
 
+  int *counter = reinterpret_cast<int *>(hist) + (tid & 3);
   uint32_t least = 0;
   int want = a.keep, total = 0;  // want: of the ranks that begin with least's digits
   if (segments == 1) load(0);
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
     constexpr int kShift[3] = {21, 10, 0}, kAbove[3] = {32, 21, 10};
-    hist[tid] = 0;
-    hist[tid + kChooseThreads] = 0;
+    hist[tid] = hist[tid + kChooseThreads] = I4{0, 0, 0, 0};
     __syncthreads();
     for (int segment = 0; segment < segments; ++segment) {
       if (segments > 1) load(segment);
@@ -427,13 +439,14 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(Choose a) {
         for (int k = 0; k < 4; ++k) {
           const uint32_t r = rank[i][k];
           const bool in = pass == 0 ? r != 0 : (r >> kAbove[pass]) == (least >> kAbove[pass]);
-          if (in) atomicAdd(&hist[(r >> kShift[pass]) & (pass == 2 ? 1023 : kBins - 1)], 1);
+          if (in) atomicAdd(counter + 4 * ((r >> kShift[pass]) & (pass == 2 ? 1023 : kBins - 1)), 1);
         }
       }
     }
     __syncthreads();
     // Bins from the highest: a thread has two.
-    const int high = hist[kBins - 1 - 2 * tid], low = hist[kBins - 2 - 2 * tid];
+    const I4 h4 = hist[kBins - 1 - 2 * tid], l4 = hist[kBins - 2 - 2 * tid];
+    const int high = (h4[0] + h4[1]) + (h4[2] + h4[3]), low = (l4[0] + l4[1]) + (l4[2] + l4[3]);
     int upto = wave_scan(high + low);
     if (lane == 63) waves[wave] = upto;
     __syncthreads();
@@ -461,31 +474,32 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(Choose a) {
   if (all) least = 1, want = total;  // every token, those of rank 1 in order
   int32_t *out = a.index + (static_cast<int64_t>(b) * a.c.heads + h) * a.keep;
   int done = 0, ties = 0;  // tokens over the least rank and at it, of earlier segments
-  const uint64_t below = (uint64_t{1} << lane) - 1;
   for (int segment = 0; segment < segments && a.keep > 0; ++segment) {
     if (segments > 1) load(segment);
     __syncthreads();  // base has been read
+    int upto[kLoads];  // tokens over the least rank of the lanes up to this one, and at it, in 16 bits each
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      int over = 0, at = 0;
+      int count = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        over += __popcll(__ballot(rank[i][k] > least));
-        at += __popcll(__ballot(rank[i][k] == least));
+        count += rank[i][k] > least ? 1 : 0;
+        count += rank[i][k] == least ? 1 << 16 : 0;
       }
-      if (lane == 0) {
-        base[0][i * kChooseWaves + wave] = over;
-        base[1][i * kChooseWaves + wave] = at;
+      upto[i] = wave_scan(count);
+      if (lane == 63) {
+        base[0][i * kChooseWaves + wave] = upto[i] & 0xffff;
+        base[1][i * kChooseWaves + wave] = upto[i] >> 16;
       }
+      upto[i] -= count;
     }
     __syncthreads();
     if (wave < 2) {  // sums in front of each
       int carry = wave == 0 ? done : ties;
       for (int i = 0; i < kLoads * kChooseWaves; i += 64) {
-        const bool in = i + lane < kLoads * kChooseWaves;
-        const int v = in ? base[wave][i + lane] : 0, upto = wave_scan(v);
-        if (in) base[wave][i + lane] = carry + upto - v;
-        carry += __builtin_amdgcn_readlane(upto, 63);
+        const int v = base[wave][i + lane], sum = wave_scan(v);
+        base[wave][i + lane] = carry + sum - v;
+        carry += __builtin_amdgcn_readlane(sum, 63);
       }
       if (lane == 0) pick[wave] = carry;
     }
@@ -494,19 +508,16 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(Choose a) {
     ties = pick[1];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      int over = base[0][i * kChooseWaves + wave], at = base[1][i * kChooseWaves + wave];
+      const int t = segment * kSegment + i * (4 * kChooseThreads) + 4 * tid;
+      int over = base[0][i * kChooseWaves + wave] + (upto[i] & 0xffff), at = base[1][i * kChooseWaves + wave] + (upto[i] >> 16);
+      // Over the least rank, then those at it that are wanted: `over` counts both.
+      at = at < want ? at : want;
+      over += at;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        over += __popcll(__ballot(rank[i][k] > least) & below);
-        at += __popcll(__ballot(rank[i][k] == least) & below);
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t r = rank[i][k];
-        if (r > least || (r == least && at < want))
-          out[over + (at < want ? at : want)] = segment * kSegment + i * (4 * kChooseThreads) + 4 * tid + k;
-        over += r > least;
-        at += r == least;
+        const bool tie = rank[i][k] == least && at < want;
+        if (rank[i][k] > least || tie) out[over++] = t + k;
+        at += tie;
       }
     }
   }
