@@ -435,6 +435,12 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(Choose a) {
       if (segments > 1) load(segment);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
+        if (pass == 2) {  // few waves still have one
+          bool any = false;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) any |= (rank[i][k] >> kAbove[pass]) == (least >> kAbove[pass]);
+          if (!__any(any)) continue;
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint32_t r = rank[i][k];
