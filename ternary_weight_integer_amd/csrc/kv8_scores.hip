@@ -40,7 +40,7 @@ struct Weigh {
 };
 
 constexpr int kBlockTokens = 256, kStage = 64;
-constexpr int kLeastStages = 4;  // of a part
+constexpr int kLeastStages = 2;  // of a part
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -93,10 +93,11 @@ __device__ inline f32x4 product(f16x8 q, f16x8 k, f32x4 f) { return __builtin_am
 __device__ inline f32x4 product(bf16x8 q, bf16x8 k, f32x4 f) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(q, k, f, 0, 0, 0); }
 
 template <typename T, int kChunks, bool kFull, bool kShaped>
-__global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) weigh_kernel(Weigh a) {
+__global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 : 4) weigh_kernel(Weigh a) {
   typedef typename std::conditional<std::is_same<T, bf16>::value, bf16x8, f16x8>::type Op;
   typedef typename Row<T>::Vec Vec;
-  constexpr int kVecs = 16 / Row<T>::kValues, kTerms = std::is_same<T, float>::value ? 2 : 1, kTiles = 4;
+  constexpr int kTerms = std::is_same<T, float>::value ? 2 : 1, kTiles = 4;
+  constexpr int kLoads = 16 * kChunks / Row<T>::kValues;  // of 16 bytes, of a lane and row
   __shared__ Op op[kTiles][kChunks][2][kTerms][64];
   __shared__ f32x4 factor[kTiles][4], less[kTiles][4], slope[kShaped ? kTiles : 1][4];
   __shared__ i32x4 place[kTiles][4];
@@ -142,8 +143,9 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) weigh_kernel(We
       }
     }
 
-    // Row n of the wave's tile of a stage.
-    Vec qv[kChunks][kVecs];
+    // Row n of the wave's tile of a stage: lane g takes 16 bytes of every 64, so
+    // that a load's four lanes of a row are neighbours.
+    Vec qv[kLoads];
     float lse;
     int i, hq;
     bool live;
@@ -153,55 +155,56 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : 2) weigh_kernel(We
       i = a.by_group.of(live ? row : r.lo);
       hq = h * a.group + (live ? row : r.lo) - i * a.group;
       lse = a.lse[static_cast<int64_t>(p.first + i) * a.q_heads + hq];
-      const T *src = static_cast<const T *>(a.q) + (p.first + i) * a.q_stride + static_cast<int64_t>(hq) * D + 16 * g;
+      const T *src = static_cast<const T *>(a.q) + (p.first + i) * a.q_stride + static_cast<int64_t>(hq) * D;
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-#pragma unroll
-        for (int k = 0; k < kVecs; ++k) {
-          qv[c][k] = Vec{};
-          if (kFull || 64 * c + 16 * g < D) qv[c][k] = reinterpret_cast<const Vec *>(src + 64 * c)[k];
-        }
+      for (int k = 0; k < kLoads; ++k) {
+        const int d = (4 * k + g) * Row<T>::kValues;
+        qv[k] = Vec{};
+        if (kFull || d < D) qv[k] = *reinterpret_cast<const Vec *>(src + d);
       }
     };
     auto lay_down = [&]() {
       const bool adds = live && fabsf(lse) < INFINITY;
+      if (__any(!adds)) {
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) qv[k] = adds ? qv[k] : Vec{};
+      }
       float qs = a.scale;
       if constexpr (kTerms == 2) {
-        float v[kChunks][16], amax = 0.0f, nan = 0.0f;
+        float amax = 0.0f;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
+        for (int k = 0; k < kLoads; ++k) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            v[c][k] = adds ? qv[c][k / 4][k % 4] : 0.0f;
-            amax = fmaxf(amax, fabsf(v[c][k]));
-            nan = fmaf(v[c][k], 0.0f, nan);
-          }
+          for (int m = 0; m < 4; ++m) amax = fmaxf(amax, fabsf(qv[k][m]));
         }
-        if (nan != 0.0f) amax = INFINITY;
         amax = over_lanes_max(amax);
+        // amax <= 127/128 2^over: an f16 is below 2^15.  A NaN or an infinity
+        // makes its row's products NaN.
         const int shift = 14 - __builtin_amdgcn_frexp_expf(amax * 0.504f);
-        qs = amax < INFINITY ? ldexpf(qs, -shift) : NAN;
+        qs = ldexpf(qs, -shift);
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
+        for (int k = 0; k < kLoads; ++k) {
+          // Components 16 k + 4 g ..: of chunk k / 4 and of lane 16 (k % 4) + n
+          // there, half g / 2, its lower or upper four.
+          union {
+            f16x2 pair[2];
+            f32x2 all;
+          } term[2];
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            f16x8 term[2];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float y = ldexpf(v[c][8 * z + k], shift);
-              term[0][k] = static_cast<f16>(y);
-              term[1][k] = static_cast<f16>(y - static_cast<float>(term[0][k]));
-            }
-            op[wave][c][z][0][lane] = term[0];
-            op[wave][c][z][1][lane] = term[1];
+          for (int m = 0; m < 2; ++m) {
+            const float y0 = ldexpf(qv[k][2 * m], shift), y1 = ldexpf(qv[k][2 * m + 1], shift);
+            term[0].pair[m] = f16x2{static_cast<f16>(y0), static_cast<f16>(y1)};
+            term[1].pair[m] = rest_of(y0, y1, term[0].pair[m]);
           }
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            reinterpret_cast<f32x2 *>(&op[wave][k / 4][g >> 1][m][16 * (k % 4) + n])[g & 1] = term[m].all;
         }
       } else {
+        // Components 32 k + 8 g ..: lane 16 (2 (k % 2) + g / 2) + n, half g % 2.
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-#pragma unroll
-          for (int z = 0; z < 2; ++z) op[wave][c][z][0][lane] = adds ? __builtin_bit_cast(Op, qv[c][z]) : Op{};
-        }
+        for (int k = 0; k < kLoads; ++k)
+          op[wave][k / 2][g & 1][0][16 * (2 * (k % 2) + (g >> 1)) + n] = __builtin_bit_cast(Op, qv[k]);
       }
       if (g == 0) {
         reinterpret_cast<float *>(factor)[16 * wave + n] = adds ? qs : 0.0f;
@@ -864,7 +867,7 @@ struct WeighPlan {
     blocks = pieces_of((tokens_of(batch, c, s) + kBlockTokens - 1) / kBlockTokens, each);
     // Parts for about eight workgroups a compute unit.
     const int64_t stages = (static_cast<int64_t>(s.rows) * (q_heads / c.heads) + kStage - 1) / kStage;
-    int64_t wanted = 8 * kUnits / (each * blocks);
+    int64_t wanted = 16 * kUnits / (each * blocks);
     if (wanted > stages / kLeastStages) wanted = stages / kLeastStages;
     parts = wanted > 1 ? static_cast<int>(wanted) : 1;
     bytes = parts > 1 ? sizeof(float) * kBlockTokens * parts * each * blocks : 0;
