@@ -124,24 +124,11 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 :
     if (part > 0 && first >= last) continue;
     if (r.stages == 0 && t1 <= own) continue;  // behind every row's window
 
-    // The wave's tokens: lane's own is tw + lane; those of a 16-token tile share a page.
+    // The wave's tokens: lane's own is tw + lane; those of a 16-token tile share a
+    // page.  Loads in the order of their uses: pages, queries, then what waits for
+    // the pages.
     const int tw = t0 + 64 * wave, tl = tw + lane;
-    const int page = tl < top ? page_of(a.s, b, tl >> a.c.lp, a.c.pages) : -1;
-    const float scale = a.c.k_scale[static_cast<int64_t>(page < 0 ? 0 : page) * a.c.heads + h];
-    float ks[4];
-    i32x4 codes[4][kChunks];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int at = __builtin_amdgcn_readlane(page, 16 * j);
-      ks[j] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(scale), 16 * j));
-      const int slot = (tw + 16 * j) & ((1 << a.c.lp) - 1);
-      const int8_t *k = a.c.k + (((static_cast<int64_t>(at < 0 ? 0 : at) * a.c.heads + h) << a.c.lp) + slot + n) * D + 16 * g;
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        codes[j][c] = i32x4{0, 0, 0, 0};
-        if (kFull || 64 * c + 16 * g < D) codes[j][c] = *reinterpret_cast<const i32x4 *>(k + 64 * c);
-      }
-    }
+    const int entry = a.s.table[b * a.s.table_stride + ((tl < top ? tl : top - 1) >> a.c.lp)];
 
     // Row n of the wave's tile of a stage: lane g takes 16 bytes of every 64, so
     // that a load's four lanes of a row are neighbours.
@@ -149,6 +136,7 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 :
     float lse;
     int i, hq;
     bool live;
+    auto has_rows = [&](int stage) { return r.lo + stage * kStage + 16 * wave < r.hi; };
     auto load = [&](int stage) {
       const int row = r.lo + stage * kStage + 16 * wave + n;
       live = row < r.hi;
@@ -214,19 +202,36 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 :
       }
     };
 
-    float total[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (first < last) load(first);
-    Op kop[4][kChunks][2];
+    if (first < last && has_rows(first)) load(first);
+    const int page = tl < top && static_cast<unsigned>(entry) < static_cast<unsigned>(a.c.pages) ? entry : -1;
+    const float scale = a.c.k_scale[static_cast<int64_t>(page < 0 ? 0 : page) * a.c.heads + h];
+    i32x4 codes[4][kChunks];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      const int at = __builtin_amdgcn_readlane(page, 16 * j);
+      const int slot = (tw + 16 * j) & ((1 << a.c.lp) - 1);
+      const int8_t *k = a.c.k + (((static_cast<int64_t>(at < 0 ? 0 : at) * a.c.heads + h) << a.c.lp) + slot + n) * D + 16 * g;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        codes[j][c] = i32x4{0, 0, 0, 0};
+        if (kFull || 64 * c + 16 * g < D) codes[j][c] = *reinterpret_cast<const i32x4 *>(k + 64 * c);
+      }
+    }
+
+    float total[4] = {0.0f, 0.0f, 0.0f, 0.0f}, ks[4];
+    Op kop[4][kChunks][2];
+    __syncthreads();  // the block before has been read
+    if (first < last && has_rows(first)) lay_down();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      ks[j] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(scale), 16 * j));
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) operands_of(codes[j][c], kop[j][c]);
     }
     for (int stage = first; stage < last; ++stage) {
+      const bool more = stage + 1 < last && has_rows(stage + 1);
       __syncthreads();
-      lay_down();
-      __syncthreads();
-      if (stage + 1 < last) load(stage + 1);
+      if (more) load(stage + 1);
       float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       for (int tile = 0; tile < kTiles; ++tile) {
         const int row = r.lo + stage * kStage + 16 * tile;
@@ -286,6 +291,8 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 :
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) total[j] += sum[j];
+      __syncthreads();
+      if (more) lay_down();
     }
     float w = 0.0f;
 #pragma unroll
