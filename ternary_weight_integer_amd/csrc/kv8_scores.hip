@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads) weigh_join_kernel(Weigh a) {
 // ---------------------------------------------------------------------------
 // The choice of the tokens that stay.
 
-constexpr int kChooseThreads = 1024, kChooseWaves = kChooseThreads / 64, kBins = 2048;
+constexpr int kBins = 2048;
 
 struct Choose {
   Cache c;
@@ -385,9 +385,9 @@ __device__ inline int wave_scan(int v) {
 // few exponents, and lanes that add to one counter take turns.
 // A sequence is one compute unit's work, bound by its vector instructions: ranks,
 // histograms and places.
-template <int kLoads>
+template <int kChooseThreads, int kLoads>
 __global__ void __launch_bounds__(kChooseThreads) choose_kernel(Choose a) {
-  constexpr int kSegment = kLoads * kChooseThreads * 4;
+  constexpr int kChooseWaves = kChooseThreads / 64, kSegment = kLoads * kChooseThreads * 4, kMine = kBins / kChooseThreads;
   typedef float F4 __attribute__((ext_vector_type(4), aligned(4)));
   typedef int I4 __attribute__((ext_vector_type(4)));
   __shared__ I4 hist[kBins];
@@ -439,7 +439,8 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(Choose a) {
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
     constexpr int kShift[3] = {21, 10, 0}, kAbove[3] = {32, 21, 10};
-    hist[tid] = hist[tid + kChooseThreads] = I4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) hist[tid + i * kChooseThreads] = I4{0, 0, 0, 0};
     __syncthreads();
     for (int segment = 0; segment < segments; ++segment) {
       if (segments > 1) load(segment);
@@ -460,10 +461,15 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(Choose a) {
       }
     }
     __syncthreads();
-    // Bins from the highest: a thread has two.
-    const I4 h4 = hist[kBins - 1 - 2 * tid], l4 = hist[kBins - 2 - 2 * tid];
-    const int high = (h4[0] + h4[1]) + (h4[2] + h4[3]), low = (l4[0] + l4[1]) + (l4[2] + l4[3]);
-    int upto = wave_scan(high + low);
+    // Bins from the highest: a thread has kMine.
+    int bins[kMine], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const I4 four = hist[kBins - 1 - i - kMine * tid];
+      bins[i] = (four[0] + four[1]) + (four[2] + four[3]);
+      mine += bins[i];
+    }
+    int upto = wave_scan(mine);
     if (lane == 63) waves[wave] = upto;
     __syncthreads();
     int sum = 0;
@@ -476,11 +482,16 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(Choose a) {
       total = sum;
       if (total <= a.keep) break;
     }
-    const int before = upto - high - low;
+    int before = upto - mine;
     if (before < want && want <= upto) {
-      const bool in_high = want <= before + high;
-      pick[0] = kBins - 1 - 2 * tid - (in_high ? 0 : 1);
-      pick[1] = want - before - (in_high ? 0 : high);
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        if (before < want && want <= before + bins[i]) {
+          pick[0] = kBins - 1 - i - kMine * tid;
+          pick[1] = want - before;
+        }
+        before += bins[i];
+      }
     }
     __syncthreads();
     least |= static_cast<uint32_t>(pick[0]) << kShift[pass];
@@ -513,8 +524,9 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(Choose a) {
     if (wave < 2) {  // sums in front of each
       int carry = wave == 0 ? done : ties;
       for (int i = 0; i < kLoads * kChooseWaves; i += 64) {
-        const int v = base[wave][i + lane], sum = wave_scan(v);
-        base[wave][i + lane] = carry + sum - v;
+        const bool in = i + lane < kLoads * kChooseWaves;
+        const int v = in ? base[wave][i + lane] : 0, sum = wave_scan(v);
+        if (in) base[wave][i + lane] = carry + sum - v;
         carry += __builtin_amdgcn_readlane(sum, 63);
       }
       if (lane == 0) pick[wave] = carry;
@@ -876,6 +888,7 @@ struct WeighPlan {
     const int64_t stages = (static_cast<int64_t>(s.rows) * (q_heads / c.heads) + kStage - 1) / kStage;
     int64_t wanted = 16 * kUnits / (each * blocks);
     if (wanted > stages / kLeastStages) wanted = stages / kLeastStages;
+    if (stages <= kLeastStages * s.seqs) wanted = 1;  // on average there is nothing to split, and a join takes 5 us
     parts = wanted > 1 ? static_cast<int>(wanted) : 1;
     bytes = parts > 1 ? sizeof(float) * kBlockTokens * parts * each * blocks : 0;
   }
@@ -978,11 +991,12 @@ extern "C" int kv8_choose(const kv8_cache *cache, const kv8_batch *batch, const 
   a.index = index;
   a.kept = kept;
   const int64_t tokens = tokens_of(batch, a.c, a.s);
-  auto launch = [&](auto kernel) {
-    kernel<<<static_cast<unsigned>(a.s.seqs * a.c.heads), kChooseThreads, 0, static_cast<hipStream_t>(stream)>>>(a);
+  auto launch = [&](auto kernel, int threads) {
+    kernel<<<static_cast<unsigned>(a.s.seqs * a.c.heads), threads, 0, static_cast<hipStream_t>(stream)>>>(a);
     return hip_status();
   };
-  return tokens <= 4 * 4096 ? launch(choose_kernel<4>) : launch(choose_kernel<16>);
+  return tokens <= 4096 ? launch(choose_kernel<256, 4>, 256)
+         : tokens <= 16384 ? launch(choose_kernel<1024, 4>, 1024) : launch(choose_kernel<1024, 16>, 1024);
 }
 
 extern "C" int kv8_move(const kv8_cache *cache, const kv8_batch *batch, const int32_t *index, const int32_t *kept, int64_t keep,
