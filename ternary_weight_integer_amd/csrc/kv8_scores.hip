@@ -995,8 +995,15 @@ extern "C" int kv8_choose(const kv8_cache *cache, const kv8_batch *batch, const 
     kernel<<<static_cast<unsigned>(a.s.seqs * a.c.heads), threads, 0, static_cast<hipStream_t>(stream)>>>(a);
     return hip_status();
   };
-  return tokens <= 4096 ? launch(choose_kernel<256, 4>, 256)
-         : tokens <= 16384 ? launch(choose_kernel<1024, 4>, 1024) : launch(choose_kernel<1024, 16>, 1024);
+  // As few threads as keep 16 or 32 ranks each: their barriers are the cheaper
+  // (384 sequences and heads of up to 4000 tokens 11.0 us with 256 threads, 19.8
+  // with 1024; 1024 of up to 8000 19.7 with 512, 40.2).  32 ranks where there is
+  // a workgroup for every unit (384 of up to 9000 17.1 against 20.9 us, but 2 of
+  // up to 16000 12.3 against 11.0).
+  if (tokens <= 4096) return launch(choose_kernel<256, 4>, 256);
+  if (tokens <= 8192) return launch(choose_kernel<512, 4>, 512);
+  if (tokens > 16384) return launch(choose_kernel<1024, 16>, 1024);
+  return a.s.seqs * a.c.heads > kUnits ? launch(choose_kernel<512, 8>, 512) : launch(choose_kernel<1024, 4>, 1024);
 }
 
 extern "C" int kv8_move(const kv8_cache *cache, const kv8_batch *batch, const int32_t *index, const int32_t *kept, int64_t keep,

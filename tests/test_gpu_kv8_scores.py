@@ -425,3 +425,32 @@ def test_a_run_that_weighs_evicts_and_goes_on():
     for _ in range(6):
         w.ref.lens = w.ref.lens + 1
         step([1, 1])
+
+
+@pytest.mark.parametrize("lens,keep", [
+    ([4096, 4097, 3000], 1000),            # 16 tokens a lane, 256 or 512 lanes
+    ([8192, 8193], 8000),
+    ([16384, 100], 2000),
+    ([16385, 65536], 30000),               # 64 tokens a lane
+    ([65537, 140000, 5], 50001),           # in segments
+])
+def test_choose_long(lens, keep):
+    """On both sides of each size of workgroup, and past the longest one's."""
+    w = World(keep, 2, 16, 64, lens, [0] * len(lens), holes=0.02)
+    m = np.exp(2 * w.rng.normal(size=(w.ref.pages, 2, 64))).astype(np.float32)
+    m[w.rng.random(m.shape) < 0.3] = 0.0
+    m[w.rng.random(m.shape) < 0.2] = np.float32(0.75)
+    want = plain.choose(w.ref, m, keep, 5, 700)
+    for bound in (max(lens), 0, 10):
+        w.batch = kv8.KV8Batch(w.batch.table, w.batch.lens, w.batch.starts, max_len=bound)
+        say(f"choose lens={lens} keep={keep} max_len={bound}")
+        for a, b in zip(kv8_scores.kv8_choose(w.cache, w.batch, dev(m), keep, first=5, recent=700), want):
+            assert np.array_equal(host(a), b)
+
+
+def test_choose_of_many_sequences():
+    w = World(77, 8, 16, 64, list(range(8300, 8300 + 40 * 40, 40)), [0] * 40)
+    m = w.rng.exponential(size=(w.ref.pages, 8, 64)).astype(np.float32)
+    want = plain.choose(w.ref, m, 1500, 4, 64)
+    for a, b in zip(kv8_scores.kv8_choose(w.cache, w.batch, dev(m), 1500, first=4, recent=64), want):
+        assert np.array_equal(host(a), b)
