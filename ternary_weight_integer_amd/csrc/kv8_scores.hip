@@ -75,6 +75,10 @@ __device__ inline void settle_mass(const Weigh &a, int page, int h, int t, bool 
   }
 }
 
+// A BF16 query of any size keeps its products in F32's range: its codes are
+// taken 2^-32 times, the scales beside them 2^32 times.
+constexpr float kBf16Keys = 0x1p-32f;
+
 // 16 codes as two operands.
 __device__ inline void operands_of(i32x4 codes, f16x8 (&out)[2]) {
 #pragma unroll
@@ -85,7 +89,7 @@ __device__ inline void operands_of(i32x4 codes, bf16x8 (&out)[2]) {
   for (int z = 0; z < 2; ++z) {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      out[z][k] = static_cast<bf16>(static_cast<float>(static_cast<int8_t>(codes[2 * z + k / 4] >> (8 * (k % 4)))));
+      out[z][k] = static_cast<bf16>(kBf16Keys * static_cast<float>(static_cast<int8_t>(codes[2 * z + k / 4] >> (8 * (k % 4)))));
   }
 }
 
@@ -225,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 :
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       ks[j] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(scale), 16 * j));
+      if constexpr (std::is_same<T, bf16>::value) ks[j] *= 1.0f / kBf16Keys;
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) operands_of(codes[j][c], kop[j][c]);
     }
@@ -868,12 +873,8 @@ inline int64_t tokens_of(const kv8_batch *batch, const Cache &c, const Batch &s)
   return batch->max_len > 0 && batch->max_len < held ? batch->max_len : held;
 }
 
-// Workgroups for `wanted` pieces of each of `each` sequences and heads, at
-// least one: fewer where a grid could not hold them (they then take several).
-inline int pieces_of(int64_t wanted, int64_t each) {
-  const int64_t most = 0x7fffffff / (each > 0 ? each : 1);
-  return static_cast<int>(wanted < 1 ? 1 : wanted < most ? wanted : most);
-}
+// A grid has fewer than 2^32 threads.
+inline bool fits(int64_t groups, int threads) { return groups <= 0xffffffffll / threads; }
 
 // How a kv8_weigh call is laid out.
 struct WeighPlan {
@@ -883,7 +884,14 @@ struct WeighPlan {
 
   WeighPlan(const Cache &c, const Batch &s, const kv8_batch *batch, int64_t q_heads) {
     each = static_cast<int64_t>(s.seqs) * c.heads;
-    blocks = pieces_of((tokens_of(batch, c, s) + kBlockTokens - 1) / kBlockTokens, each);
+    // Workgroups for every block of tokens, or fewer, which then take several
+    // each: where a grid could not hold them, and for 16 a unit where no bound of
+    // the lengths is known (a table's rows may be far longer than a sequence).
+    int64_t most = (0xffffffffll / kThreads) / each;
+    if (batch->max_len == 0 && most > 16 * kUnits / each) most = 16 * kUnits / each;
+    int64_t all = (tokens_of(batch, c, s) + kBlockTokens - 1) / kBlockTokens;
+    if (all > most) all = most;
+    blocks = all > 1 ? static_cast<int>(all) : 1;
     // Parts for about eight workgroups a compute unit.
     const int64_t stages = (static_cast<int64_t>(s.rows) * (q_heads / c.heads) + kStage - 1) / kStage;
     int64_t wanted = 16 * kUnits / (each * blocks);
@@ -942,6 +950,7 @@ extern "C" int kv8_weigh(const kv8_cache *cache, const kv8_batch *batch, int typ
   if (!lse || !aligned(lse, 4) || !mass || !aligned(mass, 4)) return I2S_EINVAL;
   if (rows * q_heads > 0x7fffffff) return I2S_ERANGE;
   const WeighPlan p(a.c, a.s, batch, q_heads);
+  if (!fits(p.each * p.blocks * p.parts, kThreads)) return I2S_ERANGE;
   if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes || !aligned(workspace, 256))) return I2S_EWORKSPACE;
   a.q = q;
   a.lse = lse;
@@ -990,6 +999,7 @@ extern "C" int kv8_choose(const kv8_cache *cache, const kv8_batch *batch, const 
   a.recent = static_cast<int>(recent);
   a.index = index;
   a.kept = kept;
+  if (!fits(static_cast<int64_t>(a.s.seqs) * a.c.heads, 1024)) return I2S_ERANGE;
   const int64_t tokens = tokens_of(batch, a.c, a.s);
   auto launch = [&](auto kernel, int threads) {
     kernel<<<static_cast<unsigned>(a.s.seqs * a.c.heads), threads, 0, static_cast<hipStream_t>(stream)>>>(a);
@@ -1031,7 +1041,7 @@ extern "C" int kv8_move(const kv8_cache *cache, const kv8_batch *batch, const in
   a.items = places * a.blocks;
   a.waves = P * a.c.dim <= 1024 ? 1 : P * a.c.dim <= 2048 ? 2 : 4;
   const int64_t grid = (a.items * a.waves + 3) / 4;
-  if (grid > 0x7fffffff) return I2S_ERANGE;
+  if (!fits(grid, kThreads)) return I2S_ERANGE;
   auto launch = [&](auto kernel) {
     kernel<<<static_cast<unsigned>(grid), kThreads, 0, static_cast<hipStream_t>(stream)>>>(a);
   };

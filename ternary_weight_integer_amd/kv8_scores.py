@@ -146,6 +146,8 @@ def kv8_choose(cache: KV8Cache, batch: KV8Batch, mass: torch.Tensor, keep: int, 
     `recent`, then those of the largest mass."""
     on = _index(cache, batch)
     mp, at = _mass(cache, mass, on), _place(on, stream)
+    if keep < 0:
+        raise I2SError("kv8_choose", i2s.I2S_EINVAL)
     index = _dense(at, (batch.seqs, cache.heads, keep), torch.int32, cache.device) if index is None else index
     kept = _dense(at, (batch.seqs,), torch.int32, cache.device) if kept is None else kept
     ip, kp = _on(index, torch.int32, (batch.seqs, cache.heads, keep), on, "index"), _on(kept, torch.int32, (batch.seqs,), on, "kept")
