@@ -14,14 +14,15 @@ namespace {
 // The weight that rows give the cached tokens.
 //
 // A workgroup owns 256 tokens of a sequence and head, a wave 64 of them, as the
-// columns of S = Q K^T: their codes stay in registers, turned into f16 or bf16
-// once (both hold them exactly), and the rows that see any of them pass by in
+// columns of S = Q K^T: their codes stay in registers, turned into f16 once (which
+// holds them exactly), and the rows that see any of them pass by in
 // stages of 64 through shared memory, where each wave lays down 16 rows.  Lane
 // (n, g) gets the logits of token n of a 16-token tile and rows 4 g .. 4 g + 3,
 // so a token's sum stays in its lane until the end.  Tokens that are none need
 // no mask: nothing of their columns is written.
-// Queries: F16 and BF16 are operands as they are, an F32 query, brought to 2^15
-// by a power of two, is the sum of two f16 (22 bits).
+// Queries: F16 is an operand as it is, BF16 is exact when brought to 2^15 by a
+// power of two (to 2^-40 of the row's largest magnitude), F32 is then the sum of
+// two f16 (22 bits).
 // Few token blocks are split along their rows into parts of whole stages; the
 // parts' sums are joined in order.
 
@@ -41,8 +42,6 @@ struct Weigh {
 
 constexpr int kBlockTokens = 256, kStage = 64;
 constexpr int kLeastStages = 2;  // of a part
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // Rows [lo, hi) of a sequence see tokens of a block, in `stages` stages, of
 // which a part has `each`.
@@ -75,30 +74,9 @@ __device__ inline void settle_mass(const Weigh &a, int page, int h, int t, bool 
   }
 }
 
-// A BF16 query of any size keeps its products in F32's range: its codes are
-// taken 2^-32 times, the scales beside them 2^32 times.
-constexpr float kBf16Keys = 0x1p-32f;
-
-// 16 codes as two operands.
-__device__ inline void operands_of(i32x4 codes, f16x8 (&out)[2]) {
-#pragma unroll
-  for (int z = 0; z < 2; ++z) out[z] = codes_to_f16(codes[2 * z], codes[2 * z + 1]);
-}
-__device__ inline void operands_of(i32x4 codes, bf16x8 (&out)[2]) {
-#pragma unroll
-  for (int z = 0; z < 2; ++z) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      out[z][k] = static_cast<bf16>(kBf16Keys * static_cast<float>(static_cast<int8_t>(codes[2 * z + k / 4] >> (8 * (k % 4)))));
-  }
-}
-
-__device__ inline f32x4 product(f16x8 q, f16x8 k, f32x4 f) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(q, k, f, 0, 0, 0); }
-__device__ inline f32x4 product(bf16x8 q, bf16x8 k, f32x4 f) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(q, k, f, 0, 0, 0); }
-
 template <typename T, int kChunks, bool kFull, bool kShaped>
 __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 : 4) weigh_kernel(Weigh a) {
-  typedef typename std::conditional<std::is_same<T, bf16>::value, bf16x8, f16x8>::type Op;
+  typedef f16x8 Op;
   typedef typename Row<T>::Vec Vec;
   constexpr int kTerms = std::is_same<T, float>::value ? 2 : 1, kTiles = 4;
   constexpr int kLoads = 16 * kChunks / Row<T>::kValues;  // of 16 bytes, of a lane and row
@@ -162,18 +140,21 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 :
         for (int k = 0; k < kLoads; ++k) qv[k] = adds ? qv[k] : Vec{};
       }
       float qs = a.scale;
-      if constexpr (kTerms == 2) {
+      int shift = 0;
+      if constexpr (!std::is_same<T, f16>::value) {
         float amax = 0.0f;
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
 #pragma unroll
-          for (int m = 0; m < 4; ++m) amax = fmaxf(amax, fabsf(qv[k][m]));
+          for (int m = 0; m < Row<T>::kValues; ++m) amax = fmaxf(amax, fabsf(static_cast<float>(qv[k][m])));
         }
         amax = over_lanes_max(amax);
         // amax <= 127/128 2^over: an f16 is below 2^15.  A NaN or an infinity
         // makes its row's products NaN.
-        const int shift = 14 - __builtin_amdgcn_frexp_expf(amax * 0.504f);
+        shift = 14 - __builtin_amdgcn_frexp_expf(amax * 0.504f);
         qs = ldexpf(qs, -shift);
+      }
+      if constexpr (kTerms == 2) {
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
           // Components 16 k + 4 g ..: of chunk k / 4 and of lane 16 (k % 4) + n
@@ -195,8 +176,16 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 :
       } else {
         // Components 32 k + 8 g ..: lane 16 (2 (k % 2) + g / 2) + n, half g % 2.
 #pragma unroll
-        for (int k = 0; k < kLoads; ++k)
-          op[wave][k / 2][g & 1][0][16 * (2 * (k % 2) + (g >> 1)) + n] = __builtin_bit_cast(Op, qv[k]);
+        for (int k = 0; k < kLoads; ++k) {
+          f16x8 term;
+          if constexpr (std::is_same<T, f16>::value) {
+            term = qv[k];
+          } else {
+#pragma unroll
+            for (int m = 0; m < 8; ++m) term[m] = static_cast<f16>(ldexpf(static_cast<float>(qv[k][m]), shift));
+          }
+          op[wave][k / 2][g & 1][0][16 * (2 * (k % 2) + (g >> 1)) + n] = term;
+        }
       }
       if (g == 0) {
         reinterpret_cast<float *>(factor)[16 * wave + n] = adds ? qs : 0.0f;
@@ -229,9 +218,11 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 :
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       ks[j] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(scale), 16 * j));
-      if constexpr (std::is_same<T, bf16>::value) ks[j] *= 1.0f / kBf16Keys;
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) operands_of(codes[j][c], kop[j][c]);
+      for (int c = 0; c < kChunks; ++c) {
+#pragma unroll
+        for (int z = 0; z < 2; ++z) kop[j][c][z] = codes_to_f16(codes[j][c][2 * z], codes[j][c][2 * z + 1]);
+      }
     }
     for (int stage = first; stage < last; ++stage) {
       const bool more = stage + 1 < last && has_rows(stage + 1);
@@ -258,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 :
             for (int m = 0; m < kTerms; ++m) {
               const Op q = op[tile][c][z][m][lane];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) f[j] = product(q, kop[j][c][z], f[j]);
+              for (int j = 0; j < 4; ++j) f[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q, kop[j][c][z], f[j], 0, 0, 0);
             }
           }
         }
