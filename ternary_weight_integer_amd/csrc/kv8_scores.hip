@@ -315,6 +315,219 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 :
   }
 }
 
+// Few rows (a decode step): a workgroup keeps a stage of rows in shared memory
+// and walks blocks of tokens, `blocks` apart; a wave's codes of the next block are
+// loaded into the registers that its products have just left, the pages are
+// looked up one block further ahead, and no wave waits for another.  Rows past a
+// stage are another walk, whose weights are added to the first one's.
+template <typename T, int kChunks, bool kFull, bool kShaped>
+__global__ void __launch_bounds__(kThreads, (kChunks > 2 ? 2 : 4)) weigh_few_kernel(Weigh a) {
+  typedef f16x8 Op;
+  typedef typename Row<T>::Vec Vec;
+  constexpr int kTerms = std::is_same<T, float>::value ? 2 : 1, kTiles = 4;
+  constexpr int kLoads = 16 * kChunks / Row<T>::kValues;  // of 16 bytes, of a lane and row
+  __shared__ Op op[kTiles][kChunks][2][kTerms][64];
+  __shared__ f32x4 factor[kTiles][4], less[kTiles][4], slope[kShaped ? kTiles : 1][4];
+  __shared__ i32x4 place[kTiles][4];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+  const int D = kFull ? 64 * kChunks : a.c.dim;
+  const int x = a.c.by_heads.of(blockIdx.x), h = blockIdx.x - x * a.c.heads;
+  const int b = a.by_blocks.of(x), block0 = x - b * a.blocks;
+  const Span p = span_of(a.s, b);
+  const int64_t held = static_cast<int64_t>(a.s.blocks) << a.c.lp;
+  const int top = held < p.len ? static_cast<int>(held) : p.len, own = p.len - p.n;
+  const int prefix = a.prefix ? a.prefix[b] : 0;
+  // The first block that the first row sees of, where there is a window.
+  const int64_t seen = a.window > 0 ? static_cast<int64_t>(own) - a.window + 1 : 0;
+  const int64_t begin = (seen > 0 ? seen & -kBlockTokens : 0) + static_cast<int64_t>(block0) * kBlockTokens;
+  if (p.n == 0 || begin >= top) return;
+  const int rows = p.n * a.group, pages = a.c.pages;
+  const int64_t stride = static_cast<int64_t>(a.blocks) * kBlockTokens;
+  const int32_t *table = a.s.table + b * a.s.table_stride;
+  const int64_t far = a.window > 0 ? a.window : INT64_C(1) << 40;
+
+  for (int row0 = 0; row0 < rows; row0 += kStage) {
+    __syncthreads();  // the stage before has been read
+    if (row0 + 16 * wave < rows) {
+      const int row = row0 + 16 * wave + n;
+      const bool live = row < rows;
+      const int i = a.by_group.of(live ? row : row0), hq = h * a.group + (live ? row : row0) - i * a.group;
+      const float lse = a.lse[static_cast<int64_t>(p.first + i) * a.q_heads + hq];
+      Vec qv[kLoads];
+      const T *src = static_cast<const T *>(a.q) + (p.first + i) * a.q_stride + static_cast<int64_t>(hq) * D;
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        const int d = (4 * k + g) * Row<T>::kValues;
+        qv[k] = Vec{};
+        if (kFull || d < D) qv[k] = *reinterpret_cast<const Vec *>(src + d);
+      }
+      const bool adds = live && fabsf(lse) < INFINITY;
+      if (__any(!adds)) {
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) qv[k] = adds ? qv[k] : Vec{};
+      }
+      float qs = a.scale;
+      int shift = 0;
+      if constexpr (!std::is_same<T, f16>::value) {
+        float amax = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+#pragma unroll
+          for (int m = 0; m < Row<T>::kValues; ++m) amax = fmaxf(amax, fabsf(static_cast<float>(qv[k][m])));
+        }
+        amax = over_lanes_max(amax);
+        // amax <= 127/128 2^over: an f16 is below 2^15.  A NaN or an infinity
+        // makes its row's products NaN.
+        shift = 14 - __builtin_amdgcn_frexp_expf(amax * 0.504f);
+        qs = ldexpf(qs, -shift);
+      }
+      if constexpr (kTerms == 2) {
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+          // Components 16 k + 4 g ..: of chunk k / 4 and of lane 16 (k % 4) + n
+          // there, half g / 2, its lower or upper four.
+          union {
+            f16x2 pair[2];
+            f32x2 all;
+          } term[2];
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const float y0 = ldexpf(qv[k][2 * m], shift), y1 = ldexpf(qv[k][2 * m + 1], shift);
+            term[0].pair[m] = f16x2{static_cast<f16>(y0), static_cast<f16>(y1)};
+            term[1].pair[m] = rest_of(y0, y1, term[0].pair[m]);
+          }
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            reinterpret_cast<f32x2 *>(&op[wave][k / 4][g >> 1][m][16 * (k % 4) + n])[g & 1] = term[m].all;
+        }
+      } else {
+        // Components 32 k + 8 g ..: lane 16 (2 (k % 2) + g / 2) + n, half g % 2.
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+          f16x8 term;
+          if constexpr (std::is_same<T, f16>::value) {
+            term = qv[k];
+          } else {
+#pragma unroll
+            for (int m = 0; m < 8; ++m) term[m] = static_cast<f16>(ldexpf(static_cast<float>(qv[k][m]), shift));
+          }
+          op[wave][k / 2][g & 1][0][16 * (2 * (k % 2) + (g >> 1)) + n] = term;
+        }
+      }
+      if (g == 0) {
+        reinterpret_cast<float *>(factor)[16 * wave + n] = adds ? qs : 0.0f;
+        reinterpret_cast<float *>(less)[16 * wave + n] = adds ? -lse * kLog2e : -INFINITY;
+        reinterpret_cast<int *>(place)[16 * wave + n] = own + i;
+        if constexpr (kShaped) reinterpret_cast<float *>(slope)[16 * wave + n] = a.slopes ? a.slopes[hq] * kLog2e : 0.0f;
+      }
+    }
+    __syncthreads();
+    const int tiles = (rows - row0 + 15) / 16 < kTiles ? (rows - row0 + 15) / 16 : kTiles;
+    int64_t t0 = begin + 64 * wave;
+    if (t0 >= top) continue;
+    auto entry_of = [&](int64_t t) { return table[((t + lane < top ? static_cast<int>(t) + lane : top - 1)) >> a.c.lp]; };
+    int page = entry_of(t0), then = entry_of(t0 + stride);
+    float scale;
+    i32x4 codes[4][kChunks];
+    auto fetch = [&](int64_t t) {
+      page = t + lane < top && static_cast<unsigned>(page) < static_cast<unsigned>(pages) ? page : -1;
+      scale = a.c.k_scale[static_cast<int64_t>(page < 0 ? 0 : page) * a.c.heads + h];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int at = __builtin_amdgcn_readlane(page, 16 * j);
+        const int slot = (static_cast<int>(t) + 16 * j) & ((1 << a.c.lp) - 1);
+        const int8_t *k = a.c.k + (((static_cast<int64_t>(at < 0 ? 0 : at) * a.c.heads + h) << a.c.lp) + slot + n) * D + 16 * g;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          codes[j][c] = i32x4{0, 0, 0, 0};
+          if (kFull || 64 * c + 16 * g < D) codes[j][c] = *reinterpret_cast<const i32x4 *>(k + 64 * c);
+        }
+      }
+    };
+    fetch(t0);
+    while (true) {
+      const int tw = static_cast<int>(t0), mine = page, tend = tw + 64 < top ? tw + 64 : top;
+      float ks[4], total[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ks[j] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(scale), 16 * j));
+      for (int tile = 0; tile < tiles; ++tile) {
+        const int row = row0 + 16 * tile;
+        const int p0 = own + a.by_group.of(row), p1 = own + a.by_group.of(row + 15 < rows ? row + 15 : rows - 1);
+        const bool early = tend <= prefix || !a.causal;  // in front of what all rows see
+        const bool none = (!early && tw >= prefix && tw > p1) || tend - 1 <= p0 - far;  // no row sees any
+        const bool edge = (!early && tend - 1 > p0) || tw <= p1 - far;
+        f32x4 f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (!none) {
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              Op q[kTerms];
+#pragma unroll
+              for (int m = 0; m < kTerms; ++m) q[m] = op[tile][c][z][m][lane];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const Op k = codes_to_f16(codes[j][c][2 * z], codes[j][c][2 * z + 1]);
+#pragma unroll
+                for (int m = 0; m < kTerms; ++m) f[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q[m], k, f[j], 0, 0, 0);
+              }
+            }
+          }
+        }
+        if (tile + 1 == tiles && t0 + stride < top) {
+          page = then;
+          fetch(t0 + stride);
+          then = entry_of(t0 + 2 * stride);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (none) continue;
+        const f32x4 qs = factor[tile][g], off = less[tile][g];
+        float e[16];
+        if constexpr (kShaped) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) e[k] = f[k / 4][k % 4] * (qs[k % 4] * ks[k / 4]);
+          if (a.cap > 0.0f) capped(e, a.cap, a.icap);
+          if (a.slopes) {
+            const f32x4 down = slope[tile][g];
+            const i32x4 pos = place[tile][g];
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              e[k] = fmaf(-down[k % 4], fabsf(static_cast<float>(sub_sat(pos[k % 4], tw + 16 * (k / 4) + n))), e[k]);
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) e[k] += off[k % 4];
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) e[k] = fmaf(f[k / 4][k % 4], qs[k % 4] * ks[k / 4], off[k % 4]);
+        }
+        if (edge) {
+          const i32x4 pos = place[tile][g];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int t = tw + 16 * (k / 4) + n, at = pos[k % 4];
+            const bool seen = (!a.causal || t <= at || t < prefix) && t > at - far;
+            e[k] = seen ? e[k] : -INFINITY;
+            asm volatile("" : "+v"(e[k]));  // keeps this a branch: few tiles take it
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) total[k / 4] += __builtin_amdgcn_exp2f(e[k]);
+      }
+      float w = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float v = over_lanes_sum(total[j]);
+        w = g == j ? v : w;
+      }
+      if (mine >= 0) settle_mass(a, mine, h, tw + lane, row0 == 0 && tw + lane >= own, w);
+      t0 += stride;
+      if (t0 >= top) break;
+    }
+  }
+}
+
 // Joins the parts of token blocks that were split: a workgroup has 64 tokens, 16
 // teams of 16 lanes sum every 16th part (a thread a token and all parts in turn
 // took 19 us for a prompt of 4096, 64 parts).
@@ -878,10 +1091,13 @@ inline int64_t tokens_of(const kv8_batch *batch, const Cache &c, const Batch &s)
 // A grid has fewer than 2^32 threads.
 inline bool fits(int64_t groups, int threads) { return groups <= 0xffffffffll / threads; }
 
+constexpr int kFewGroups = 16;
+
 // How a kv8_weigh call is laid out.
 struct WeighPlan {
   int64_t each;  // sequences and heads
   int blocks, parts;
+  bool few;
   size_t bytes;
 
   WeighPlan(const Cache &c, const Batch &s, const kv8_batch *batch, int64_t q_heads) {
@@ -893,12 +1109,15 @@ struct WeighPlan {
     if (batch->max_len == 0 && most > 16 * kUnits / each) most = 16 * kUnits / each;
     int64_t all = (tokens_of(batch, c, s) + kBlockTokens - 1) / kBlockTokens;
     if (all > most) all = most;
+    // Few rows: workgroups that walk several blocks.
+    few = static_cast<int64_t>(s.rows) * (q_heads / c.heads) <= 16 * static_cast<int64_t>(s.seqs);
+    if (few && all > kFewGroups * kUnits / each) all = kFewGroups * kUnits / each;
     blocks = all > 1 ? static_cast<int>(all) : 1;
     // Parts for about eight workgroups a compute unit.
     const int64_t stages = (static_cast<int64_t>(s.rows) * (q_heads / c.heads) + kStage - 1) / kStage;
     int64_t wanted = 16 * kUnits / (each * blocks);
     if (wanted > stages / kLeastStages) wanted = stages / kLeastStages;
-    if (stages <= kLeastStages * s.seqs) wanted = 1;  // on average there is nothing to split, and a join takes 5 us
+    if (few || stages <= kLeastStages * s.seqs) wanted = 1;  // on average there is nothing to split, and a join takes 5 us
     parts = wanted > 1 ? static_cast<int>(wanted) : 1;
     bytes = parts > 1 ? sizeof(float) * kBlockTokens * parts * each * blocks : 0;
   }
@@ -907,10 +1126,11 @@ struct WeighPlan {
 template <typename T, int kChunks, bool kFull>
 int launch_weigh(const WeighPlan &p, const Weigh &a, hipStream_t stream) {
   const unsigned grid = static_cast<unsigned>(p.each * p.blocks * p.parts);
+  auto launch = [&](auto kernel) { kernel<<<grid, kThreads, 0, stream>>>(a); };
   if (a.cap > 0.0f || a.slopes) {
-    weigh_kernel<T, kChunks, kFull, true><<<grid, kThreads, 0, stream>>>(a);
+    launch(p.few ? weigh_few_kernel<T, kChunks, kFull, true> : weigh_kernel<T, kChunks, kFull, true>);
   } else {
-    weigh_kernel<T, kChunks, kFull, false><<<grid, kThreads, 0, stream>>>(a);
+    launch(p.few ? weigh_few_kernel<T, kChunks, kFull, false> : weigh_kernel<T, kChunks, kFull, false>);
   }
   return hip_status();
 }
