@@ -84,15 +84,152 @@ __device__ inline void settle_mass(const Weigh &a, int page, int h, int t, bool 
   }
 }
 
-template <typename T, int kChunks, bool kFull, bool kShaped>
-__global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 : 4) weigh_kernel(Weigh a) {
+// A row on its way to shared memory: lane g takes 16 bytes of every 64, so that a
+// load's four lanes of a row are neighbours.
+template <typename T, int kChunks>
+struct Queries {
+  typedef typename Row<T>::Vec Vec;
+  static constexpr int kLoads = 16 * kChunks / Row<T>::kValues;
+  Vec q[kLoads];
+  float lse;
+  int i, hq;  // query token of the sequence, query head
+  bool live;
+
+  // Row `row` of the sequence's rows below `end`, for row0 one of them.
+  __device__ void load(const Weigh &a, const Span &p, int h, int D, int row, int end, int row0) {
+    const int g = (threadIdx.x & 63) >> 4;
+    live = row < end;
+    i = a.by_group.of(live ? row : row0);
+    hq = h * a.group + (live ? row : row0) - i * a.group;
+    lse = a.lse[static_cast<int64_t>(p.first + i) * a.q_heads + hq];
+    const T *src = static_cast<const T *>(a.q) + (p.first + i) * a.q_stride + static_cast<int64_t>(hq) * D;
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      const int d = (4 * k + g) * Row<T>::kValues;
+      q[k] = Vec{};
+      if (d < D) q[k] = *reinterpret_cast<const Vec *>(src + d);
+    }
+  }
+};
+
+// A stage's rows in shared memory, as operands, and what their weights take.
+template <typename T, int kChunks, bool kShaped>
+struct Stage {
+  static constexpr int kTerms = std::is_same<T, float>::value ? 2 : 1, kTiles = 4;
   typedef f16x8 Op;
   typedef typename Row<T>::Vec Vec;
-  constexpr int kTerms = std::is_same<T, float>::value ? 2 : 1, kTiles = 4;
-  constexpr int kLoads = 16 * kChunks / Row<T>::kValues;  // of 16 bytes, of a lane and row
-  __shared__ Op op[kTiles][kChunks][2][kTerms][64];
-  __shared__ f32x4 factor[kTiles][4], less[kTiles][4], slope[kShaped ? kTiles : 1][4];
-  __shared__ i32x4 place[kTiles][4];
+  static constexpr int kLoads = Queries<T, kChunks>::kLoads;
+  Op op[kTiles][kChunks][2][kTerms][64];
+  f32x4 factor[kTiles][4], less[kTiles][4], slope[kShaped ? kTiles : 1][4];
+  i32x4 place[kTiles][4];
+
+  // The wave's rows to tile `tile`.
+  __device__ void lay_down(const Weigh &a, Queries<T, kChunks> &row, int tile, int own) {
+    const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+    const bool adds = row.live && fabsf(row.lse) < INFINITY;
+    if (__any(!adds)) {
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) row.q[k] = adds ? row.q[k] : Vec{};
+    }
+    float qs = a.scale;
+    int shift = 0;
+    if constexpr (!std::is_same<T, f16>::value) {
+      float amax = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+#pragma unroll
+        for (int m = 0; m < Row<T>::kValues; ++m) amax = fmaxf(amax, fabsf(static_cast<float>(row.q[k][m])));
+      }
+      amax = over_lanes_max(amax);
+      // amax <= 127/128 2^over: an f16 is below 2^15.  A NaN or an infinity
+      // makes its row's products NaN.
+      shift = 14 - __builtin_amdgcn_frexp_expf(amax * 0.504f);
+      qs = ldexpf(qs, -shift);
+    }
+    if constexpr (kTerms == 2) {
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        // Components 16 k + 4 g ..: of chunk k / 4 and of lane 16 (k % 4) + n
+        // there, half g / 2, its lower or upper four.
+        union {
+          f16x2 pair[2];
+          f32x2 all;
+        } term[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const float y0 = ldexpf(row.q[k][2 * m], shift), y1 = ldexpf(row.q[k][2 * m + 1], shift);
+          term[0].pair[m] = f16x2{static_cast<f16>(y0), static_cast<f16>(y1)};
+          term[1].pair[m] = rest_of(y0, y1, term[0].pair[m]);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          reinterpret_cast<f32x2 *>(&op[tile][k / 4][g >> 1][m][16 * (k % 4) + n])[g & 1] = term[m].all;
+      }
+    } else {
+      // Components 32 k + 8 g ..: lane 16 (2 (k % 2) + g / 2) + n, half g % 2.
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        f16x8 term;
+        if constexpr (std::is_same<T, f16>::value) {
+          term = row.q[k];
+        } else {
+#pragma unroll
+          for (int m = 0; m < 8; ++m) term[m] = static_cast<f16>(ldexpf(static_cast<float>(row.q[k][m]), shift));
+        }
+        op[tile][k / 2][g & 1][0][16 * (2 * (k % 2) + (g >> 1)) + n] = term;
+      }
+    }
+    if (g == 0) {
+      reinterpret_cast<float *>(factor)[16 * tile + n] = adds ? qs : 0.0f;
+      reinterpret_cast<float *>(less)[16 * tile + n] = adds ? -row.lse * kLog2e : -INFINITY;
+      reinterpret_cast<int *>(place)[16 * tile + n] = own + row.i;
+      if constexpr (kShaped) reinterpret_cast<float *>(slope)[16 * tile + n] = a.slopes ? a.slopes[row.hq] * kLog2e : 0.0f;
+    }
+  }
+
+  // Exponents, in units of log2, of a tile's rows 4 g .. and the tokens n of the
+  // four 16-token tiles from tw on: f their products, ks the tokens' scales.
+  // edge: some row does not see some token.
+  __device__ void exponents(const Weigh &a, int tile, const f32x4 (&f)[4], const float (&ks)[4], int tw, int prefix, int64_t far, bool edge,
+                            float (&e)[16]) const {
+    const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+    const f32x4 qs = factor[tile][g], off = less[tile][g];
+    if constexpr (kShaped) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) e[k] = f[k / 4][k % 4] * (qs[k % 4] * ks[k / 4]);
+      if (a.cap > 0.0f) capped(e, a.cap, a.icap);
+      if (a.slopes) {
+        const f32x4 down = slope[tile][g];
+        const i32x4 pos = place[tile][g];
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          e[k] = fmaf(-down[k % 4], fabsf(static_cast<float>(sub_sat(pos[k % 4], tw + 16 * (k / 4) + n))), e[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 16; ++k) e[k] += off[k % 4];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) e[k] = fmaf(f[k / 4][k % 4], qs[k % 4] * ks[k / 4], off[k % 4]);
+    }
+    if (edge) {
+      const i32x4 pos = place[tile][g];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int t = tw + 16 * (k / 4) + n, at = pos[k % 4];
+        const bool seen = (!a.causal || t <= at || t < prefix) && t > at - far;
+        e[k] = seen ? e[k] : -INFINITY;
+        asm volatile("" : "+v"(e[k]));  // keeps this a branch: few tiles take it
+      }
+    }
+  }
+};
+
+template <typename T, int kChunks, bool kFull, bool kShaped>
+__global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 : 4) weigh_kernel(Weigh a) {
+  typedef Stage<T, kChunks, kShaped> S;
+  typedef typename S::Op Op;
+  constexpr int kTerms = S::kTerms, kTiles = S::kTiles;
+  __shared__ S laid;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int D = kFull ? 64 * kChunks : a.c.dim;
   int rest = a.c.by_heads.of(blockIdx.x);
@@ -122,89 +259,10 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 :
     const int tw = t0 + 64 * wave, tl = tw + lane;
     const int entry = a.s.table[b * a.s.table_stride + ((tl < top ? tl : top - 1) >> a.c.lp)];
 
-    // Row n of the wave's tile of a stage: lane g takes 16 bytes of every 64, so
-    // that a load's four lanes of a row are neighbours.
-    Vec qv[kLoads];
-    float lse;
-    int i, hq;
-    bool live;
+    Queries<T, kChunks> row;  // n of the wave's tile of a stage
     auto has_rows = [&](int stage) { return r.lo + stage * kStage + 16 * wave < r.hi; };
-    auto load = [&](int stage) {
-      const int row = r.lo + stage * kStage + 16 * wave + n;
-      live = row < r.hi;
-      i = a.by_group.of(live ? row : r.lo);
-      hq = h * a.group + (live ? row : r.lo) - i * a.group;
-      lse = a.lse[static_cast<int64_t>(p.first + i) * a.q_heads + hq];
-      const T *src = static_cast<const T *>(a.q) + (p.first + i) * a.q_stride + static_cast<int64_t>(hq) * D;
-#pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        const int d = (4 * k + g) * Row<T>::kValues;
-        qv[k] = Vec{};
-        if (kFull || d < D) qv[k] = *reinterpret_cast<const Vec *>(src + d);
-      }
-    };
-    auto lay_down = [&]() {
-      const bool adds = live && fabsf(lse) < INFINITY;
-      if (__any(!adds)) {
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k) qv[k] = adds ? qv[k] : Vec{};
-      }
-      float qs = a.scale;
-      int shift = 0;
-      if constexpr (!std::is_same<T, f16>::value) {
-        float amax = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k) {
-#pragma unroll
-          for (int m = 0; m < Row<T>::kValues; ++m) amax = fmaxf(amax, fabsf(static_cast<float>(qv[k][m])));
-        }
-        amax = over_lanes_max(amax);
-        // amax <= 127/128 2^over: an f16 is below 2^15.  A NaN or an infinity
-        // makes its row's products NaN.
-        shift = 14 - __builtin_amdgcn_frexp_expf(amax * 0.504f);
-        qs = ldexpf(qs, -shift);
-      }
-      if constexpr (kTerms == 2) {
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k) {
-          // Components 16 k + 4 g ..: of chunk k / 4 and of lane 16 (k % 4) + n
-          // there, half g / 2, its lower or upper four.
-          union {
-            f16x2 pair[2];
-            f32x2 all;
-          } term[2];
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const float y0 = ldexpf(qv[k][2 * m], shift), y1 = ldexpf(qv[k][2 * m + 1], shift);
-            term[0].pair[m] = f16x2{static_cast<f16>(y0), static_cast<f16>(y1)};
-            term[1].pair[m] = rest_of(y0, y1, term[0].pair[m]);
-          }
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-            reinterpret_cast<f32x2 *>(&op[wave][k / 4][g >> 1][m][16 * (k % 4) + n])[g & 1] = term[m].all;
-        }
-      } else {
-        // Components 32 k + 8 g ..: lane 16 (2 (k % 2) + g / 2) + n, half g % 2.
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k) {
-          f16x8 term;
-          if constexpr (std::is_same<T, f16>::value) {
-            term = qv[k];
-          } else {
-#pragma unroll
-            for (int m = 0; m < 8; ++m) term[m] = static_cast<f16>(ldexpf(static_cast<float>(qv[k][m]), shift));
-          }
-          op[wave][k / 2][g & 1][0][16 * (2 * (k % 2) + (g >> 1)) + n] = term;
-        }
-      }
-      if (g == 0) {
-        reinterpret_cast<float *>(factor)[16 * wave + n] = adds ? qs : 0.0f;
-        reinterpret_cast<float *>(less)[16 * wave + n] = adds ? -lse * kLog2e : -INFINITY;
-        reinterpret_cast<int *>(place)[16 * wave + n] = own + i;
-        if constexpr (kShaped) reinterpret_cast<float *>(slope)[16 * wave + n] = a.slopes ? a.slopes[hq] * kLog2e : 0.0f;
-      }
-    };
-
+    auto load = [&](int stage) { row.load(a, p, h, D, r.lo + stage * kStage + 16 * wave + n, r.hi, r.lo); };
+    auto lay_down = [&]() { laid.lay_down(a, row, wave, own); };
     if (first < last && has_rows(first)) load(first);
     const int page = tl < top && static_cast<unsigned>(entry) < static_cast<unsigned>(a.c.pages) ? entry : -1;
     const float scale = a.c.k_scale[static_cast<int64_t>(page < 0 ? 0 : page) * a.c.heads + h];
@@ -240,9 +298,9 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 :
       if (more) load(stage + 1);
       float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       for (int tile = 0; tile < kTiles; ++tile) {
-        const int row = r.lo + stage * kStage + 16 * tile;
-        if (row >= r.hi || tw >= top) break;
-        const int p0 = own + a.by_group.of(row), p1 = own + a.by_group.of(row + 15 < r.hi ? row + 15 : r.hi - 1);
+        const int row0 = r.lo + stage * kStage + 16 * tile;
+        if (row0 >= r.hi || tw >= top) break;
+        const int p0 = own + a.by_group.of(row0), p1 = own + a.by_group.of(row0 + 15 < r.hi ? row0 + 15 : r.hi - 1);
         const int tend = tw + 64 < top ? tw + 64 : top;
         const bool early = tend <= prefix || !a.causal;  // in front of what all rows see
         const int64_t far = a.window > 0 ? a.window : INT64_C(1) << 40;
@@ -257,41 +315,14 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 :
           for (int z = 0; z < 2; ++z) {
 #pragma unroll
             for (int m = 0; m < kTerms; ++m) {
-              const Op q = op[tile][c][z][m][lane];
+              const Op q = laid.op[tile][c][z][m][lane];
 #pragma unroll
               for (int j = 0; j < 4; ++j) f[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q, kop[j][c][z], f[j], 0, 0, 0);
             }
           }
         }
-        const f32x4 qs = factor[tile][g], off = less[tile][g];
         float e[16];
-        if constexpr (kShaped) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) e[k] = f[k / 4][k % 4] * (qs[k % 4] * ks[k / 4]);
-          if (a.cap > 0.0f) capped(e, a.cap, a.icap);
-          if (a.slopes) {
-            const f32x4 down = slope[tile][g];
-            const i32x4 pos = place[tile][g];
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              e[k] = fmaf(-down[k % 4], fabsf(static_cast<float>(sub_sat(pos[k % 4], tw + 16 * (k / 4) + n))), e[k]);
-          }
-#pragma unroll
-          for (int k = 0; k < 16; ++k) e[k] += off[k % 4];
-        } else {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) e[k] = fmaf(f[k / 4][k % 4], qs[k % 4] * ks[k / 4], off[k % 4]);
-        }
-        if (edge) {
-          const i32x4 pos = place[tile][g];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int t = tw + 16 * (k / 4) + n, at = pos[k % 4];
-            const bool seen = (!a.causal || t <= at || t < prefix) && t > at - far;
-            e[k] = seen ? e[k] : -INFINITY;
-            asm volatile("" : "+v"(e[k]));  // keeps this a branch: few tiles take it
-          }
-        }
+        laid.exponents(a, tile, f, ks, tw, prefix, far, edge, e);
 #pragma unroll
         for (int k = 0; k < 16; ++k) sum[k / 4] += __builtin_amdgcn_exp2f(e[k]);
       }
@@ -322,13 +353,10 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 :
 // stage are another walk, whose weights are added to the first one's.
 template <typename T, int kChunks, bool kFull, bool kShaped>
 __global__ void __launch_bounds__(kThreads, (kChunks > 2 ? 2 : 4)) weigh_few_kernel(Weigh a) {
-  typedef f16x8 Op;
-  typedef typename Row<T>::Vec Vec;
-  constexpr int kTerms = std::is_same<T, float>::value ? 2 : 1, kTiles = 4;
-  constexpr int kLoads = 16 * kChunks / Row<T>::kValues;  // of 16 bytes, of a lane and row
-  __shared__ Op op[kTiles][kChunks][2][kTerms][64];
-  __shared__ f32x4 factor[kTiles][4], less[kTiles][4], slope[kShaped ? kTiles : 1][4];
-  __shared__ i32x4 place[kTiles][4];
+  typedef Stage<T, kChunks, kShaped> S;
+  typedef typename S::Op Op;
+  constexpr int kTerms = S::kTerms, kTiles = S::kTiles;
+  __shared__ S laid;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int D = kFull ? 64 * kChunks : a.c.dim;
   const int x = a.c.by_heads.of(blockIdx.x), h = blockIdx.x - x * a.c.heads;
@@ -349,77 +377,9 @@ __global__ void __launch_bounds__(kThreads, (kChunks > 2 ? 2 : 4)) weigh_few_ker
   for (int row0 = 0; row0 < rows; row0 += kStage) {
     __syncthreads();  // the stage before has been read
     if (row0 + 16 * wave < rows) {
-      const int row = row0 + 16 * wave + n;
-      const bool live = row < rows;
-      const int i = a.by_group.of(live ? row : row0), hq = h * a.group + (live ? row : row0) - i * a.group;
-      const float lse = a.lse[static_cast<int64_t>(p.first + i) * a.q_heads + hq];
-      Vec qv[kLoads];
-      const T *src = static_cast<const T *>(a.q) + (p.first + i) * a.q_stride + static_cast<int64_t>(hq) * D;
-#pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        const int d = (4 * k + g) * Row<T>::kValues;
-        qv[k] = Vec{};
-        if (kFull || d < D) qv[k] = *reinterpret_cast<const Vec *>(src + d);
-      }
-      const bool adds = live && fabsf(lse) < INFINITY;
-      if (__any(!adds)) {
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k) qv[k] = adds ? qv[k] : Vec{};
-      }
-      float qs = a.scale;
-      int shift = 0;
-      if constexpr (!std::is_same<T, f16>::value) {
-        float amax = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k) {
-#pragma unroll
-          for (int m = 0; m < Row<T>::kValues; ++m) amax = fmaxf(amax, fabsf(static_cast<float>(qv[k][m])));
-        }
-        amax = over_lanes_max(amax);
-        // amax <= 127/128 2^over: an f16 is below 2^15.  A NaN or an infinity
-        // makes its row's products NaN.
-        shift = 14 - __builtin_amdgcn_frexp_expf(amax * 0.504f);
-        qs = ldexpf(qs, -shift);
-      }
-      if constexpr (kTerms == 2) {
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k) {
-          // Components 16 k + 4 g ..: of chunk k / 4 and of lane 16 (k % 4) + n
-          // there, half g / 2, its lower or upper four.
-          union {
-            f16x2 pair[2];
-            f32x2 all;
-          } term[2];
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const float y0 = ldexpf(qv[k][2 * m], shift), y1 = ldexpf(qv[k][2 * m + 1], shift);
-            term[0].pair[m] = f16x2{static_cast<f16>(y0), static_cast<f16>(y1)};
-            term[1].pair[m] = rest_of(y0, y1, term[0].pair[m]);
-          }
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-            reinterpret_cast<f32x2 *>(&op[wave][k / 4][g >> 1][m][16 * (k % 4) + n])[g & 1] = term[m].all;
-        }
-      } else {
-        // Components 32 k + 8 g ..: lane 16 (2 (k % 2) + g / 2) + n, half g % 2.
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k) {
-          f16x8 term;
-          if constexpr (std::is_same<T, f16>::value) {
-            term = qv[k];
-          } else {
-#pragma unroll
-            for (int m = 0; m < 8; ++m) term[m] = static_cast<f16>(ldexpf(static_cast<float>(qv[k][m]), shift));
-          }
-          op[wave][k / 2][g & 1][0][16 * (2 * (k % 2) + (g >> 1)) + n] = term;
-        }
-      }
-      if (g == 0) {
-        reinterpret_cast<float *>(factor)[16 * wave + n] = adds ? qs : 0.0f;
-        reinterpret_cast<float *>(less)[16 * wave + n] = adds ? -lse * kLog2e : -INFINITY;
-        reinterpret_cast<int *>(place)[16 * wave + n] = own + i;
-        if constexpr (kShaped) reinterpret_cast<float *>(slope)[16 * wave + n] = a.slopes ? a.slopes[hq] * kLog2e : 0.0f;
-      }
+      Queries<T, kChunks> row;
+      row.load(a, p, h, D, row0 + 16 * wave + n, rows, row0);
+      laid.lay_down(a, row, wave, own);
     }
     __syncthreads();
     const int tiles = (rows - row0 + 15) / 16 < kTiles ? (rows - row0 + 15) / 16 : kTiles;
@@ -466,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, (kChunks > 2 ? 2 : 4)) weigh_few_ker
             for (int z = 0; z < 2; ++z) {
               Op q[kTerms];
 #pragma unroll
-              for (int m = 0; m < kTerms; ++m) q[m] = op[tile][c][z][m][lane];
+              for (int m = 0; m < kTerms; ++m) q[m] = laid.op[tile][c][z][m][lane];
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const Op k = codes_to_f16(codes[j][c][2 * z], codes[j][c][2 * z + 1]);
@@ -483,35 +443,8 @@ __global__ void __launch_bounds__(kThreads, (kChunks > 2 ? 2 : 4)) weigh_few_ker
           __builtin_amdgcn_sched_barrier(0);
         }
         if (none) continue;
-        const f32x4 qs = factor[tile][g], off = less[tile][g];
         float e[16];
-        if constexpr (kShaped) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) e[k] = f[k / 4][k % 4] * (qs[k % 4] * ks[k / 4]);
-          if (a.cap > 0.0f) capped(e, a.cap, a.icap);
-          if (a.slopes) {
-            const f32x4 down = slope[tile][g];
-            const i32x4 pos = place[tile][g];
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              e[k] = fmaf(-down[k % 4], fabsf(static_cast<float>(sub_sat(pos[k % 4], tw + 16 * (k / 4) + n))), e[k]);
-          }
-#pragma unroll
-          for (int k = 0; k < 16; ++k) e[k] += off[k % 4];
-        } else {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) e[k] = fmaf(f[k / 4][k % 4], qs[k % 4] * ks[k / 4], off[k % 4]);
-        }
-        if (edge) {
-          const i32x4 pos = place[tile][g];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int t = tw + 16 * (k / 4) + n, at = pos[k % 4];
-            const bool seen = (!a.causal || t <= at || t < prefix) && t > at - far;
-            e[k] = seen ? e[k] : -INFINITY;
-            asm volatile("" : "+v"(e[k]));  // keeps this a branch: few tiles take it
-          }
-        }
+        laid.exponents(a, tile, f, ks, tw, prefix, far, edge, e);
 #pragma unroll
         for (int k = 0; k < 16; ++k) total[k / 4] += __builtin_amdgcn_exp2f(e[k]);
       }
@@ -1091,6 +1024,8 @@ inline int64_t tokens_of(const kv8_batch *batch, const Cache &c, const Batch &s)
 // A grid has fewer than 2^32 threads.
 inline bool fits(int64_t groups, int threads) { return groups <= 0xffffffffll / threads; }
 
+// Workgroups a unit of calls with few rows, which are on a unit four at a time (8,
+// 12, 16 and 32: 70, 68, 67 and 69 us for the batch of 64).
 constexpr int kFewGroups = 16;
 
 // How a kv8_weigh call is laid out.

@@ -317,3 +317,22 @@ def test_nothing_kept_and_nothing_there():
     kv8_scores.kv8_weigh(w.cache, w.batch, torch.zeros((0, 4, 64), device=DEV), torch.zeros((0, 4), device=DEV), mass)
     w.same_cache()
     assert not host(mass).any()
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("D", [64, 80, 128, 256])
+def test_weigh_few_rows_on_average(D, dtype):
+    """A decode step's kernel where one sequence has several stages of rows, with windows that leave blocks behind, a prefix that
+    reaches past them, and holes."""
+    lens, news = [1300] + list(range(250, 700, 45)) * 2, [90] + [1] * 20
+    for kw in ({}, dict(window=100), dict(window=300, prefix=[1290] + [240] * 20, cap=5.0), dict(causal=False, slopes=True, holes=0.2)):
+        w = World(D, 2, D, 32, lens, news, holes=kw.pop("holes", 0.0))
+        assert w.rows * 3 <= 16 * len(lens)
+        check_weigh(w, 3, dtype, **kw)
+
+
+def test_weigh_one_row_far_behind_its_window():
+    for bound in (20000, 0):
+        w = World(27, 1, 64, 64, [20000, 90], [1, 2])
+        w.batch = kv8.KV8Batch(w.batch.table, w.batch.lens, w.batch.starts, max_len=bound)
+        check_weigh(w, 4, F32, window=700, tag="far")
