@@ -346,17 +346,20 @@ __global__ void __launch_bounds__(kThreads, kChunks > 2 ? 1 : kChunks == 2 ? 3 :
   }
 }
 
+constexpr int kHeldBlocks = 4;  // whose sums a workgroup of few rows holds over the stages
+
 // Few rows (a decode step): a workgroup keeps a stage of rows in shared memory
 // and walks blocks of tokens, `blocks` apart; a wave's codes of the next block are
 // loaded into the registers that its products have just left, the pages are
 // looked up one block further ahead, and no wave waits for another.  Rows past a
-// stage are another walk, whose weights are added to the first one's.
+// stage are another walk, over kHeldBlocks blocks at a time.
 template <typename T, int kChunks, bool kFull, bool kShaped>
 __global__ void __launch_bounds__(kThreads, (kChunks > 2 ? 2 : 4)) weigh_few_kernel(Weigh a) {
   typedef Stage<T, kChunks, kShaped> S;
   typedef typename S::Op Op;
   constexpr int kTerms = S::kTerms, kTiles = S::kTiles;
   __shared__ S laid;
+  __shared__ float held_sums[kHeldBlocks][kBlockTokens];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int D = kFull ? 64 * kChunks : a.c.dim;
   const int x = a.c.by_heads.of(blockIdx.x), h = blockIdx.x - x * a.c.heads;
@@ -374,89 +377,102 @@ __global__ void __launch_bounds__(kThreads, (kChunks > 2 ? 2 : 4)) weigh_few_ker
   const int32_t *table = a.s.table + b * a.s.table_stride;
   const int64_t far = a.window > 0 ? a.window : INT64_C(1) << 40;
 
-  for (int row0 = 0; row0 < rows; row0 += kStage) {
-    __syncthreads();  // the stage before has been read
-    if (row0 + 16 * wave < rows) {
-      Queries<T, kChunks> row;
-      row.load(a, p, h, D, row0 + 16 * wave + n, rows, row0);
-      laid.lay_down(a, row, wave, own);
-    }
-    __syncthreads();
-    const int tiles = (rows - row0 + 15) / 16 < kTiles ? (rows - row0 + 15) / 16 : kTiles;
-    int64_t t0 = begin + 64 * wave;
-    if (t0 >= top) continue;
-    auto entry_of = [&](int64_t t) { return table[((t + lane < top ? static_cast<int>(t) + lane : top - 1)) >> a.c.lp]; };
-    int page = entry_of(t0), then = entry_of(t0 + stride);
-    float scale;
-    i32x4 codes[4][kChunks];
-    auto fetch = [&](int64_t t) {
-      page = t + lane < top && static_cast<unsigned>(page) < static_cast<unsigned>(pages) ? page : -1;
-      scale = a.c.k_scale[static_cast<int64_t>(page < 0 ? 0 : page) * a.c.heads + h];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int at = __builtin_amdgcn_readlane(page, 16 * j);
-        const int slot = (static_cast<int>(t) + 16 * j) & ((1 << a.c.lp) - 1);
-        const int8_t *k = a.c.k + (((static_cast<int64_t>(at < 0 ? 0 : at) * a.c.heads + h) << a.c.lp) + slot + n) * D + 16 * g;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          codes[j][c] = i32x4{0, 0, 0, 0};
-          if (kFull || 64 * c + 16 * g < D) codes[j][c] = *reinterpret_cast<const i32x4 *>(k + 64 * c);
-        }
+  // With one stage all blocks in one go; else as many as there is room to hold the
+  // sums of, so that a token's weights reach the mass as one sum.
+  const int64_t reach = rows <= kStage ? top : kHeldBlocks * stride;
+  for (int64_t from = begin; from < top; from += reach) {
+    const int64_t end = from + reach < top ? from + reach : top;
+    for (int row0 = 0; row0 < rows; row0 += kStage) {
+      __syncthreads();  // the stage before has been read
+      if (row0 + 16 * wave < rows) {
+        Queries<T, kChunks> row;
+        row.load(a, p, h, D, row0 + 16 * wave + n, rows, row0);
+        laid.lay_down(a, row, wave, own);
       }
-    };
-    fetch(t0);
-    while (true) {
-      const int tw = static_cast<int>(t0), mine = page, tend = tw + 64 < top ? tw + 64 : top;
-      float ks[4], total[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      __syncthreads();
+      const int tiles = (rows - row0 + 15) / 16 < kTiles ? (rows - row0 + 15) / 16 : kTiles;
+      int64_t t0 = from + 64 * wave;
+      if (t0 >= end) continue;
+      int turn = 0;
+      auto entry_of = [&](int64_t t) { return table[((t + lane < top ? static_cast<int>(t) + lane : top - 1)) >> a.c.lp]; };
+      int page = entry_of(t0), then = entry_of(t0 + stride);
+      float scale;
+      i32x4 codes[4][kChunks];
+      auto fetch = [&](int64_t t) {
+        page = t + lane < top && static_cast<unsigned>(page) < static_cast<unsigned>(pages) ? page : -1;
+        scale = a.c.k_scale[static_cast<int64_t>(page < 0 ? 0 : page) * a.c.heads + h];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) ks[j] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(scale), 16 * j));
-      for (int tile = 0; tile < tiles; ++tile) {
-        const int row = row0 + 16 * tile;
-        const int p0 = own + a.by_group.of(row), p1 = own + a.by_group.of(row + 15 < rows ? row + 15 : rows - 1);
-        const bool early = tend <= prefix || !a.causal;  // in front of what all rows see
-        const bool none = (!early && tw >= prefix && tw > p1) || tend - 1 <= p0 - far;  // no row sees any
-        const bool edge = (!early && tend - 1 > p0) || tw <= p1 - far;
-        f32x4 f[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (!none) {
+        for (int j = 0; j < 4; ++j) {
+          const int at = __builtin_amdgcn_readlane(page, 16 * j);
+          const int slot = (static_cast<int>(t) + 16 * j) & ((1 << a.c.lp) - 1);
+          const int8_t *k = a.c.k + (((static_cast<int64_t>(at < 0 ? 0 : at) * a.c.heads + h) << a.c.lp) + slot + n) * D + 16 * g;
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
+            codes[j][c] = i32x4{0, 0, 0, 0};
+            if (kFull || 64 * c + 16 * g < D) codes[j][c] = *reinterpret_cast<const i32x4 *>(k + 64 * c);
+          }
+        }
+      };
+      fetch(t0);
+      while (true) {
+        const int tw = static_cast<int>(t0), mine = page, tend = tw + 64 < top ? tw + 64 : top;
+        float ks[4], total[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              Op q[kTerms];
+        for (int j = 0; j < 4; ++j) ks[j] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(scale), 16 * j));
+        for (int tile = 0; tile < tiles; ++tile) {
+          const int row = row0 + 16 * tile;
+          const int p0 = own + a.by_group.of(row), p1 = own + a.by_group.of(row + 15 < rows ? row + 15 : rows - 1);
+          const bool early = tend <= prefix || !a.causal;  // in front of what all rows see
+          const bool none = (!early && tw >= prefix && tw > p1) || tend - 1 <= p0 - far;  // no row sees any
+          const bool edge = (!early && tend - 1 > p0) || tw <= p1 - far;
+          f32x4 f[4];
 #pragma unroll
-              for (int m = 0; m < kTerms; ++m) q[m] = laid.op[tile][c][z][m][lane];
+          for (int j = 0; j < 4; ++j) f[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          if (!none) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const Op k = codes_to_f16(codes[j][c][2 * z], codes[j][c][2 * z + 1]);
+            for (int c = 0; c < kChunks; ++c) {
 #pragma unroll
-                for (int m = 0; m < kTerms; ++m) f[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q[m], k, f[j], 0, 0, 0);
+              for (int z = 0; z < 2; ++z) {
+                Op q[kTerms];
+#pragma unroll
+                for (int m = 0; m < kTerms; ++m) q[m] = laid.op[tile][c][z][m][lane];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const Op k = codes_to_f16(codes[j][c][2 * z], codes[j][c][2 * z + 1]);
+#pragma unroll
+                  for (int m = 0; m < kTerms; ++m) f[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q[m], k, f[j], 0, 0, 0);
+                }
               }
             }
           }
-        }
-        if (tile + 1 == tiles && t0 + stride < top) {
-          page = then;
-          fetch(t0 + stride);
-          then = entry_of(t0 + 2 * stride);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        if (none) continue;
-        float e[16];
-        laid.exponents(a, tile, f, ks, tw, prefix, far, edge, e);
+          if (tile + 1 == tiles && t0 + stride < end) {
+            page = then;
+            fetch(t0 + stride);
+            then = entry_of(t0 + 2 * stride);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          if (none) continue;
+          float e[16];
+          laid.exponents(a, tile, f, ks, tw, prefix, far, edge, e);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) total[k / 4] += __builtin_amdgcn_exp2f(e[k]);
-      }
-      float w = 0.0f;
+          for (int k = 0; k < 16; ++k) total[k / 4] += __builtin_amdgcn_exp2f(e[k]);
+        }
+        float w = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float v = over_lanes_sum(total[j]);
-        w = g == j ? v : w;
+        for (int j = 0; j < 4; ++j) {
+          const float v = over_lanes_sum(total[j]);
+          w = g == j ? v : w;
+        }
+        if (row0 > 0) w += held_sums[turn][threadIdx.x];
+        if (row0 + kStage < rows) {
+          held_sums[turn][threadIdx.x] = w;
+        } else if (mine >= 0) {
+          settle_mass(a, mine, h, tw + lane, tw + lane >= own, w);
+        }
+        t0 += stride;
+        if (t0 >= end) break;
+        ++turn;
       }
-      if (mine >= 0) settle_mass(a, mine, h, tw + lane, row0 == 0 && tw + lane >= own, w);
-      t0 += stride;
-      if (t0 >= top) break;
     }
   }
 }

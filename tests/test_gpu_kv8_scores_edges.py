@@ -331,6 +331,15 @@ def test_weigh_few_rows_on_average(D, dtype):
         check_weigh(w, 3, dtype, **kw)
 
 
+@pytest.mark.parametrize("dtype", [F32, F16])
+def test_weigh_many_rows_among_many_sequences(dtype):
+    """So many sequences that a workgroup takes all the blocks of one, more than it holds the sums of, and one with several stages."""
+    lens, news = [9 + i % 20 for i in range(1023)] + [2700], [1] * 1023 + [50]
+    w = World(28, 4, 64, 16, lens, news)
+    assert w.rows * 3 <= 16 * len(lens) and len(lens) * 4 >= 16 * 256
+    check_weigh(w, 3, dtype, window=2300, cap=5.0, tag="among")
+
+
 def test_weigh_one_row_far_behind_its_window():
     for bound in (20000, 0):
         w = World(27, 1, 64, 64, [20000, 90], [1, 2])
