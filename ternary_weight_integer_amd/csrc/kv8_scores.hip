@@ -26,15 +26,12 @@ namespace {
 // Few token blocks are split along their rows into parts of whole stages; the
 // parts' sums are joined in order.
 //
-// One token of each of 64 sequences of 500 to 8000 tokens, 32 query heads over 8
-// of 128, BF16: 75 us for 299 MB (4.0 TB/s), bound by how much of the cache is on
-// its way with three waves a SIMD.  A prompt of 4096 F32 rows, 12 heads over 2 of
-// 128: 82 us, 0.31 PFLOP/s of the formula's operations (two f16 a query double
-// them); matrix products take 21% of the SIMDs' cycles and vector instructions (a
-// weight's scale, exponent and sum, the queries' two parts) 40%, the rest is a
-// workgroup's begin and the barriers of its stages.  Blocks of 512 tokens (two
-// waves a SIMD, 103 us), a tile's operands read ahead (91), and, for few rows,
-// codes turned where they are used (83) were slower.
+// A prompt of 4096 F32 rows, 12 heads over 2 of 128: 81 us, 0.31 PFLOP/s of the
+// formula's operations (two f16 a query double them); matrix products take about
+// 21% of the SIMDs' cycles and vector instructions (a weight's scale, exponent and
+// sum, the queries' two parts) 40%, the rest is a workgroup's begin and the
+// barriers of its stages.  Blocks of 512 tokens (two waves a SIMD, 103 us against
+// then 82) and a tile's operands read ahead (91) were slower.
 
 struct Weigh {
   Cache c;
@@ -353,6 +350,10 @@ constexpr int kHeldBlocks = 4;  // whose sums a workgroup of few rows holds over
 // loaded into the registers that its products have just left, the pages are
 // looked up one block further ahead, and no wave waits for another.  Rows past a
 // stage are another walk, over kHeldBlocks blocks at a time.
+// One token of each of 64 sequences of 500 to 8000 tokens, 32 query heads over 8
+// of 128, BF16: 66 us for 299 MB (4.5 TB/s), bound by how much of the cache is on
+// its way with four waves a SIMD; weigh_kernel, with three and a begin for every
+// block, takes 76.
 template <typename T, int kChunks, bool kFull, bool kShaped>
 __global__ void __launch_bounds__(kThreads, (kChunks > 2 ? 2 : 4)) weigh_few_kernel(Weigh a) {
   typedef Stage<T, kChunks, kShaped> S;
@@ -1060,8 +1061,11 @@ struct WeighPlan {
     if (batch->max_len == 0 && most > 16 * kUnits / each) most = 16 * kUnits / each;
     int64_t all = (tokens_of(batch, c, s) + kBlockTokens - 1) / kBlockTokens;
     if (all > most) all = most;
-    // Few rows: workgroups that walk several blocks.
-    few = static_cast<int64_t>(s.rows) * (q_heads / c.heads) <= 16 * static_cast<int64_t>(s.seqs);
+    // Few rows, up to 32 a sequence and head on average: workgroups that walk
+    // several blocks.  64 sequences of 4000 tokens, 8 heads of 128, BF16, with 4, 16,
+    // 32, 48 and 64 rows: 47, 49, 62, 77 and 93 us against the other kernel's 55, 56,
+    // 67, 75 and 84.
+    few = static_cast<int64_t>(s.rows) * (q_heads / c.heads) <= 32 * static_cast<int64_t>(s.seqs);
     if (few && all > kFewGroups * kUnits / each) all = kFewGroups * kUnits / each;
     blocks = all > 1 ? static_cast<int>(all) : 1;
     // Parts for about eight workgroups a compute unit.
