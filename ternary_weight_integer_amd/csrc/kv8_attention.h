@@ -25,10 +25,11 @@ namespace {
 //       two (to 2^-40 of the row's largest magnitude), one of F32 is then the sum
 //       of two (22 bits).  The keys have to be turned into f16.
 //   O^T = V^T P^T  f16 16x16x32.  V's codes are exact in f16; a weight is the sum
-//     of two (22 bits), where many BF16 rows are worked on one (11 bits: its
-//     rounding is an eighth of the result's own, and adds 0.5 to 0.8% to its
-//     error; a second takes 18 to 20% of a prompt's time, and 1 to 4% where rows
-//     are few).
+//     of two (22 bits), where many BF16 rows of plain scores are worked on one (11
+//     bits: its rounding is an eighth of the result's own, and adds 0.5 to 0.8% to
+//     its error; a second takes 18 to 20% of a prompt's time, and 1 to 4% where
+//     rows are few).  Shaped scores have the second always: four capped BF16
+//     prompts of 500 to 4000 tokens, 16 heads over 8 of 128, 184 us against 163.
 // The rows of K's four 16-token operands are taken from the tile in the order
 // 16 (m / 4) + 4 j + m % 4, which leaves lane (row, g) with the logits of the
 // 16 consecutive tokens 16 g ..: those are its k indices of P^T, and one
@@ -731,10 +732,14 @@ struct Many {
   static constexpr int kGroups = kChunks > 2 ? 1 : kDirect ? 2 : 3;  // workgroups on a unit, at least
 };
 
+// f16 parts of a weight where rows are many.
+template <typename A, typename T>
+constexpr int kManyParts = std::is_same<T, bf16>::value && !std::is_same<A, Shaped>::value ? 1 : 2;
+
 template <typename A, typename T, int kChunks, bool kFull, int kRowTiles>
 __global__ void __launch_bounds__(kThreads, (Many<T, kChunks, kRowTiles>::kGroups)) attention_many_kernel(A a) {
   constexpr bool kDirect = Many<T, kChunks, kRowTiles>::kDirect;
-  typedef Rows<A, T, kChunks, kFull, kRowTiles, kDirect, std::is_same<T, bf16>::value ? 1 : 2> R;
+  typedef Rows<A, T, kChunks, kFull, kRowTiles, kDirect, kManyParts<A, T>> R;
   constexpr int kOut = R::kOut, kRows = 16 * kRowTiles, kBlock = 4 * kRows;
   __shared__ i32x4 lk[2][4][kChunks][R::kKeys][64];
   __shared__ f16x8 lv[2][kOut][2][64];
