@@ -85,6 +85,14 @@ struct Shaped : Attend {
   const int32_t *prefix;  // [seqs]
 };
 
+// v within F32's range; a NaN stays one.
+__device__ inline float in_range(float v) { return fabsf(v) == INFINITY ? copysignf(FLT_MAX, v) : v; }
+
+// A head's slope in units of log2.  One that log2 e takes out of F32's range is
+// held at its end: an infinity would make distance 0 a NaN, and one token
+// further on either's weight is 0.
+__device__ inline float slope_of(const float *slopes, int head) { return slopes ? in_range(slopes[head] * kLog2e) : 0.0f; }
+
 // Tokens in front of which rows of sequence b see all.
 __device__ inline int prefix_of(const Attend &, int) { return 0; }
 __device__ inline int prefix_of(const Shaped &a, int b) { return a.prefix ? a.prefix[b] : 0; }
@@ -345,7 +353,7 @@ struct Rows {
       head_of[t] = w.h * a.group + (live ? row - i * a.group : 0);
       hi[t] = !live ? 0 : end_of(a, pos, prefix, end);
       if constexpr (kShaped) {
-        slope[t] = a.slopes ? a.slopes[head_of[t]] * kLog2e : 0.0f;
+        slope[t] = slope_of(a.slopes, head_of[t]);
         pos_of[t] = pos;
       }
       lo[t] = a.window > 0 ? clamp_int(static_cast<int64_t>(pos) - a.window + 1, end) : 0;

@@ -180,7 +180,7 @@ struct Stage {
       reinterpret_cast<float *>(factor)[16 * tile + n] = adds ? qs : 0.0f;
       reinterpret_cast<float *>(less)[16 * tile + n] = adds ? -row.lse * kLog2e : -INFINITY;
       reinterpret_cast<int *>(place)[16 * tile + n] = own + row.i;
-      if constexpr (kShaped) reinterpret_cast<float *>(slope)[16 * tile + n] = a.slopes ? a.slopes[row.hq] * kLog2e : 0.0f;
+      if constexpr (kShaped) reinterpret_cast<float *>(slope)[16 * tile + n] = adds ? slope_of(a.slopes, row.hq) : 0.0f;
     }
   }
 

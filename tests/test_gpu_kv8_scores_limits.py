@@ -40,3 +40,37 @@ def test_bf16_prompts_are_rounded_once(lens, heads, group, kw):
     low, high = rounded(ref["out"] - tol, BF16), rounded(ref["out"] + tol, BF16)
     off = (got < low) | (got > high)
     assert not off.any(), f"{off.sum()} of {off.size} results are no rounding of the sum"
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("lens,news", [([70, 33], [1, 1]), ([200, 150], [200, 90])])
+def test_slopes_up_to_the_largest_number(lens, news, dtype):
+    """A row sees its own token, at distance 0, and the one before, whose exponent is as good as none.  Exponents are off by at most
+    (3 + 64 / 16 + 8) u spread, spread < 0.125 * 0.03 * 127 * 64 * 4 = 122: 1.1e-4, and as much of a weight."""
+    for steep in (2.5e38, np.finfo(np.float32).max):
+        for cap in (0.0, 5.0):
+            w = World(3, 2, 64, 16, lens, news)
+            q = w.values(w.rows, dtype, heads=4)
+            slopes = np.array([steep, 0.5, 0.0, steep], np.float32)
+            say(f"slopes {steep} cap={cap} lens={lens} {dtype}")
+            kw = dict(window=2, cap=cap)
+            ref = plain.attention(w.ref, q, 0.125, slopes=slopes, **kw)
+            out, lse = kv8_scores.kv8_attention_scored(w.cache, w.batch, dev(q, dtype), slopes=dev(slopes), lse=True, **kw)
+            assert np.allclose(host(lse), ref["lse"], rtol=1e-5, atol=1.2e-4)
+            assert np.allclose(host(out), ref["out"], rtol=2.0 ** -8, atol=3e-4 * np.abs(ref["mag"]).max())
+            mass = kv8_scores.new_mass(w.cache)
+            kv8_scores.kv8_weigh(w.cache, w.batch, dev(q, dtype), lse, mass, slopes=dev(slopes), **kw)
+            want, _ = plain.weigh(w.ref, q, host(lse), np.zeros(mass.shape, np.float32), 0.125, slopes=slopes, **kw)
+            assert np.allclose(host(mass), want, rtol=1.5e-4, atol=1e-6)
+
+
+def test_rows_that_add_nothing_whatever_their_slope():
+    w = World(5, 2, 64, 16, [200], [3])
+    q, lse = w.values(3, F32, heads=4), np.full((3, 4), 3.0, np.float32)
+    lse[:, 1] = [np.nan, -np.inf, np.inf]
+    for steep in (3e38, -3e38):
+        slopes, mass = np.array([0.5, steep, 0.25, 0.125], np.float32), kv8_scores.new_mass(w.cache)
+        kv8_scores.kv8_weigh(w.cache, w.batch, dev(q), dev(lse), mass, slopes=dev(slopes))
+        with np.errstate(invalid="ignore"):
+            want, _ = plain.weigh(w.ref, q, lse, np.zeros(mass.shape, np.float32), 0.125, slopes=slopes)
+        assert np.allclose(host(mass), want, rtol=1.5e-4, atol=1e-6)
