@@ -18,13 +18,13 @@
  *   e_t = e_t - slopes[h] * |p - t|        where slopes are given
  * and t is seen if t < L, and t <= p or t < prefix[b] where causal (prefix
  * NULL: 0), and t > p - window where window > 0.
- *   scale    finite.
+ *   scale    within +-2^126.
  *   window   >= 0.
  *   cap      0 (none), or 2^-60 .. 2^60.
  *   slopes   NULL, or F32 [q_heads], finite.
  *   prefix   NULL, or int32 [seqs] (a negative one counts as 0).
  * Exponents e_t and the lse are F32: they resolve to their last bit, and have to
- * stay in its range (before the cap, where there is one, they need not).
+ * stay within +-2^127 (before the cap, where there is one, they need not).
  * Positions are places in the cache.  After kv8_move they are the places that
  * the chosen tokens then have: windows, distances and prefixes go by those,
  * and rotated keys keep the angles of the positions that they were written at.

@@ -407,6 +407,7 @@ struct Rows {
       const int over = __builtin_amdgcn_frexp_expf(amax * 0.504f) + 1;
       const int shift = !kDirect ? 8 * kDigits - 1 - over : std::is_same<T, f16>::value ? 0 : 15 - over;
       qs[t] = amax < INFINITY ? ldexpf(a.scale, -shift) : NAN;
+      if constexpr (kShaped) qs[t] = in_range(qs[t]);
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         if constexpr (kDirect) {
@@ -477,8 +478,11 @@ struct Rows {
   __device__ void weigh(int t, const f32x4 (&f)[4], const Scales &s, int first, bool edge, Weights (&w)[kParts]) {
     if constexpr (kShaped) {
       float x[16];
+      // Before a cap a score may be past F32's range.  Its factor is held to it,
+      // so that a dot of 0 stays 0; the least other, 2^-24, is past every cap.
+      const float factor = in_range(qs[t] * s.ks);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) x[k] = f[k / 4][k % 4] * (qs[t] * s.ks);
+      for (int k = 0; k < 16; ++k) x[k] = f[k / 4][k % 4] * factor;
       if (a.cap > 0.0f) capped(x, a.cap, a.icap);
       if (a.slopes) {
         const float away = static_cast<float>(sub_sat(pos_of[t], first));

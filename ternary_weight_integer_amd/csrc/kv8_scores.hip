@@ -177,7 +177,7 @@ struct Stage {
       }
     }
     if (g == 0) {
-      reinterpret_cast<float *>(factor)[16 * tile + n] = adds ? qs : 0.0f;
+      reinterpret_cast<float *>(factor)[16 * tile + n] = adds ? kShaped ? in_range(qs) : qs : 0.0f;
       reinterpret_cast<float *>(less)[16 * tile + n] = adds ? -row.lse * kLog2e : -INFINITY;
       reinterpret_cast<int *>(place)[16 * tile + n] = own + row.i;
       if constexpr (kShaped) reinterpret_cast<float *>(slope)[16 * tile + n] = adds ? slope_of(a.slopes, row.hq) : 0.0f;
@@ -192,8 +192,9 @@ struct Stage {
     const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
     const f32x4 qs = factor[tile][g], off = less[tile][g];
     if constexpr (kShaped) {
+      // Before a cap a score may be past F32's range: see Rows::weigh.
 #pragma unroll
-      for (int k = 0; k < 16; ++k) e[k] = f[k / 4][k % 4] * (qs[k % 4] * ks[k / 4]);
+      for (int k = 0; k < 16; ++k) e[k] = f[k / 4][k % 4] * __builtin_amdgcn_fmed3f(qs[k % 4] * ks[k / 4], -FLT_MAX, FLT_MAX);
       if (a.cap > 0.0f) capped(e, a.cap, a.icap);
       if (a.slopes) {
         const f32x4 down = slope[tile][g];
@@ -1025,9 +1026,10 @@ __global__ void __launch_bounds__(kThreads) move_kernel(Move a) {
 // ---------------------------------------------------------------------------
 // Host side.
 
-// I2S_OK, or what is wrong with the scores' shape.
+// I2S_OK, or what is wrong with the scores' shape.  A scale within 2^126 is one
+// in units of log2, too.
 inline int check_shape(float scale, int64_t window, float cap, const float *slopes, const int32_t *prefix) {
-  if (window < 0 || !(fabsf(scale) < INFINITY)) return I2S_EINVAL;
+  if (window < 0 || !(fabsf(scale) <= 0x1p126f)) return I2S_EINVAL;
   if (!(cap == 0.0f || (cap >= 0x1p-60f && cap <= 0x1p60f)) || !aligned(slopes, 4) || !aligned(prefix, 4)) return I2S_EINVAL;
   return I2S_OK;
 }

@@ -74,3 +74,37 @@ def test_rows_that_add_nothing_whatever_their_slope():
         with np.errstate(invalid="ignore"):
             want, _ = plain.weigh(w.ref, q, lse, np.zeros(mass.shape, np.float32), 0.125, slopes=slopes)
         assert np.allclose(host(mass), want, rtol=1.5e-4, atol=1e-6)
+
+
+@pytest.mark.parametrize("dtype,size,scale,ks", [
+    (F32, 1e20, 1e36, 0.02),      # the row's factor past F32's range
+    (F32, 1.0, 1e36, 1e5),        # its product with a key's scale
+    (F32, 1e38, 2.0 ** 126, 1e35),
+    (F16, 6e4, 1e36, 1e5),
+    (BF16, 1e30, -1e36, 0.02),
+    (BF16, 1.0, 1e36, 1e5),
+])
+@pytest.mark.parametrize("lens,news", [([70, 33], [1, 1]), ([200, 150], [200, 90])])
+def test_a_key_of_zeros_under_scores_past_the_range(lens, news, dtype, size, scale, ks):
+    """Scores of any size are capped, one of 0 stays 0: every third key is zeros, and one page has the scale 0.  Scores
+    are 0 or the cap, so exponents are off by 10 u of it and by 8 u (2 * 5 + 25), 2e-5, and a sum of 200 adds 1.2e-5."""
+    D, cap = 64, 5.0
+    w = World(4, 2, D, 16, lens, news)
+    w.ref.k[:, :, ::3] = 0
+    w.ref.ks[:] = np.float32(ks)
+    w.ref.ks[w.ref.table[0, 1]] = 0.0
+    w.cache.k.copy_(dev(w.ref.k))
+    w.cache.k_scale.copy_(dev(w.ref.ks))
+    # One component a query, so that a dot is no difference of large terms.
+    q = np.zeros((w.rows, 4, D), np.float32)
+    q[:, :, 7] = np.where(w.rng.random((w.rows, 4)) < 0.5, -1, 1) * size
+    q = rounded(q, dtype)
+    say(f"past the range: size={size} scale={scale} ks={ks} lens={lens} {dtype}")
+    ref = plain.attention(w.ref, q, scale, cap=cap)
+    out, lse = kv8_scores.kv8_attention_scored(w.cache, w.batch, dev(q, dtype), scale=scale, cap=cap, lse=True)
+    assert np.allclose(host(lse), ref["lse"], rtol=1e-5, atol=3.2e-5)
+    assert np.allclose(host(out), ref["out"], rtol=2.0 ** -8, atol=1e-4 * np.abs(ref["mag"]).max())
+    mass = kv8_scores.new_mass(w.cache)
+    kv8_scores.kv8_weigh(w.cache, w.batch, dev(q, dtype), lse, mass, scale=scale, cap=cap)
+    want, _ = plain.weigh(w.ref, q, host(lse), np.zeros(mass.shape, np.float32), scale, cap=cap)
+    assert np.allclose(host(mass), want, rtol=5e-5, atol=1e-7)
