@@ -67,7 +67,11 @@ size_t kv8_weigh_workspace_bytes(const kv8_cache *cache, const kv8_batch *batch,
  *         of exp(e_t - lse[i][h])
  *   mass_t = w_t for the call's own tokens (those at positions L - n_b and on),
  *            mass_t + w_t for earlier ones,
- * so the masses of a page need no clearing when its first token is appended.
+ * Where every token that is appended is a row of one such call, masses need no
+ * clearing when a page is begun.  Where some are not (only a prompt's last rows
+ * are weighed, or not every step's), theirs are added to from the first call on:
+ * the caller sets their masses to 0 before it (a whole page's when it is begun,
+ * by an append or a move), else what the page held before counts as theirs.
  *   q, q_stride, q_heads, rows   the queries, as kv8_attention's.
  *   lse      F32 [rows][q_heads], as the attention with the same scores wrote
  *            it.  A row and head whose lse is not finite (it saw nothing, its

@@ -125,7 +125,9 @@ def kv8_weigh(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, lse: torch.Tens
     """Add the attention weight that rows q [rows][q_heads][dim], with the lse
     F32 [rows][q_heads] of the attention with the same scores, give each cached
     token to mass F32 [pages][heads][page_tokens]; masses of the call's own
-    tokens are set to it."""
+    tokens are set to it.  Tokens that no call has as rows (a prompt's before
+    its last ones) are added to what their pages' masses hold: mass[pages] = 0
+    where such a page is begun."""
     index = _index(cache, batch)
     code = _type(q, "q")
     qp, qs, q_heads, rows = _heads(q, None, cache.dim, q.dtype, index, "q")

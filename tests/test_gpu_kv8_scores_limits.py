@@ -108,3 +108,25 @@ def test_a_key_of_zeros_under_scores_past_the_range(lens, news, dtype, size, sca
     kv8_scores.kv8_weigh(w.cache, w.batch, dev(q, dtype), lse, mass, scale=scale, cap=cap)
     want, _ = plain.weigh(w.ref, q, host(lse), np.zeros(mass.shape, np.float32), scale, cap=cap)
     assert np.allclose(host(mass), want, rtol=5e-5, atol=1e-7)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_prompt_of_which_only_the_last_rows_are_weighed(dtype):
+    """Its pages are taken anew and hold another sequence's masses: they are added to where they are left, and count for nothing where
+    they are zeroed as the header asks, up to the choice."""
+    w = World(6, 2, 64, 16, [250, 37], [32, 32])
+    q = w.values(w.rows, dtype, heads=8)
+    _, lse = kv8.kv8_attention(w.cache, w.batch, dev(q, dtype), lse=True)
+    old = (1000 * w.rng.exponential(size=(w.ref.pages, 2, 16))).astype(np.float32)
+    begun = [int(p) for b, n in enumerate(w.ref.lens) for p in w.ref.table[b, :-(-int(n) // 16)]]
+    for zeroed in (False, True):
+        if zeroed:
+            old[begun] = 0.0
+        mass = dev(old)
+        kv8_scores.kv8_weigh(w.cache, w.batch, dev(q, dtype), lse, mass)
+        bound = noise(64, dtype)
+        want, off = plain.weigh(w.ref, q, host(lse), old, 0.125, noise=lambda parts, spread, s: bound(parts, spread) + 8 * U * parts
+                                + 4 * U * np.abs(s) + 8 * U)
+        assert (np.abs(host(mass) - want) <= off + 1e-37).all()
+        got = kv8_scores.kv8_choose(w.cache, w.batch, mass, 60, first=2, recent=8)
+        assert all(np.array_equal(host(a), b) for a, b in zip(got, plain.choose(w.ref, host(mass), 60, 2, 8)))
