@@ -5,8 +5,12 @@ from __future__ import annotations
 
 import pytest
 
-from ternary_weight_integer_amd import i2s
-from test_abi_kv8_scores_cpu import scored, weigh
+from ternary_weight_integer_amd import i2s, kv8_scores
+from test_abi_kv8_scores_cpu import FAKE, _batch, _cache, _ref, scored, weigh
+
+
+def weigh_workspace_bytes(cache, batch, rows):
+    return kv8_scores.lib().kv8_weigh_workspace_bytes(_ref(cache), _ref(batch), 12, rows)
 
 
 @pytest.mark.parametrize("fn", [scored, weigh])
@@ -16,3 +20,20 @@ def test_scales(fn):
         assert fn(scale=scale, rows=0) == i2s.I2S_OK
     for scale in (2.4e38, -3.4e38):
         assert fn(scale=scale) == i2s.I2S_EINVAL
+
+
+@pytest.mark.parametrize("seqs,blocks,rows", [(1, 64, 4096), (3, 20, 3 * 200)])
+def test_weigh_workspace(seqs, blocks, rows):
+    """Rows that several workgroups share: a workspace of the size asked for, aligned, or none of the call runs."""
+    batch = _batch(table_stride=blocks, blocks=blocks, starts=None, seqs=seqs, max_len=64 * blocks)
+    need = weigh_workspace_bytes(_cache(), batch, rows)
+    assert need > 0 and need % 1024 == 0
+    for kw in (dict(workspace=None), dict(workspace=FAKE + 128), dict(workspace_bytes=need - 1), dict(workspace_bytes=0)):
+        assert weigh(batch=batch, rows=rows, **kw) == i2s.I2S_EWORKSPACE
+
+
+def test_weigh_without_a_workspace():
+    """None where a sequence's rows are a stage or two, and for arguments that are refused."""
+    for seqs, rows in ((1, 1), (64, 64), (4, 80)):
+        assert weigh_workspace_bytes(_cache(), _batch(starts=None, seqs=seqs), rows) == 0
+    assert weigh_workspace_bytes(_cache(dim=120), _batch(), 4096) == weigh_workspace_bytes(_cache(), _batch(), -1) == 0

@@ -9,7 +9,8 @@ import numpy as np
 import pytest
 import torch
 
-from ternary_weight_integer_amd import kv8, kv8_scores
+from ternary_weight_integer_amd import i2s, kv8, kv8_scores
+from ternary_weight_integer_amd.i2s import I2SError
 
 pytestmark = pytest.mark.gpu
 
@@ -17,7 +18,7 @@ if not torch.cuda.is_available():
     pytest.skip("no GPU visible", allow_module_level=True)
 
 import kv8_plain as plain  # noqa: E402
-from test_gpu_kv8 import BF16, F16, F32, U, World, dev, host, rounded, say  # noqa: E402
+from test_gpu_kv8 import BF16, DEV, F16, F32, U, World, dev, host, rounded, say  # noqa: E402
 from test_gpu_kv8_scores import noise, shape_of  # noqa: E402
 
 
@@ -130,3 +131,45 @@ def test_a_prompt_of_which_only_the_last_rows_are_weighed(dtype):
         assert (np.abs(host(mass) - want) <= off + 1e-37).all()
         got = kv8_scores.kv8_choose(w.cache, w.batch, mass, 60, first=2, recent=8)
         assert all(np.array_equal(host(a), b) for a, b in zip(got, plain.choose(w.ref, host(mass), 60, 2, 8)))
+
+
+def guarded(size):
+    """(workspace of `size` bytes that are NaN, all of what it lies in)."""
+    whole = torch.full((256 + size + 256,), 0xFF, dtype=torch.uint8, device=DEV)
+    assert whole.data_ptr() % 256 == 0
+    return whole[256:256 + size], whole
+
+
+@pytest.mark.parametrize("lens,news,bound", [([4096], [4096], 4096), ([900, 1300, 64, 0], [300, 250, 64, 0], 1300), ([3000], [700], 500)])
+def test_workspaces_of_the_size_asked_for(lens, news, bound):
+    """Nothing is written beside them, nothing is read of them that the call has not written, and one byte less is refused."""
+    w = World(8, 2, 128, 64, lens, news)
+    w.batch = kv8.KV8Batch(w.batch.table, w.batch.lens, w.batch.starts, max_len=bound)
+    q = dev(w.values(w.rows, F32, heads=12))
+    _, lse = kv8.kv8_attention(w.cache, w.batch, q, lse=True)
+    size = kv8_scores.kv8_weigh_workspace_bytes(w.cache, w.batch, 12, w.rows)
+    say(f"workspace lens={lens} bytes={size}")
+    assert size > 0
+    workspace, whole = guarded(size)
+    masses = [kv8_scores.new_mass(w.cache) for _ in range(3)]
+    kv8_scores.kv8_weigh(w.cache, w.batch, q, lse, masses[0], workspace=workspace)
+    kv8_scores.kv8_weigh(w.cache, w.batch, q, lse, masses[1])
+    assert torch.equal(masses[0], masses[1]) and host(masses[0]).sum() > 0
+    edge = host(whole)
+    assert (edge[:256] == 0xFF).all() and (edge[-256:] == 0xFF).all()
+    with pytest.raises(I2SError) as refused:
+        kv8_scores.kv8_weigh(w.cache, w.batch, q, lse, masses[2], workspace=workspace[:-1])
+    assert refused.value.status == i2s.I2S_EWORKSPACE and not host(masses[2]).any()
+
+
+@pytest.mark.parametrize("lens,news", [([5000], [1]), ([3000, 20], [40, 2])])
+def test_scored_attention_in_a_workspace_of_the_size_asked_for(lens, news):
+    w = World(9, 2, 128, 64, lens, news)
+    q = dev(w.values(w.rows, F32, heads=12))
+    size = kv8.kv8_attention_workspace_bytes(w.cache, w.batch, 12, w.rows)
+    assert size > 0
+    workspace, whole = guarded(size)
+    want = kv8_scores.kv8_attention_scored(w.cache, w.batch, q, cap=9.0, lse=True)
+    got = kv8_scores.kv8_attention_scored(w.cache, w.batch, q, cap=9.0, lse=True, workspace=workspace)
+    edge = host(whole)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and (edge[:256] == 0xFF).all() and (edge[-256:] == 0xFF).all()
