@@ -70,6 +70,13 @@ def _workspace(workspace, need: int, index: int, at, device):
     return workspace, workspace.data_ptr(), workspace.numel()
 
 
+def _cap(fn: str, cap: float) -> float:
+    """A cap that F32 rounds to 0 is refused as the library refuses all below 2^-60: 0 is none."""
+    if cap and not ctypes.c_float(cap).value:
+        raise I2SError(fn, i2s.I2S_EINVAL)
+    return cap
+
+
 def _shape(batch: KV8Batch, q_heads: int, slopes, prefix, index: int):
     """Pointers of the scores' slopes and prefix."""
     return (None if slopes is None else _on(slopes, torch.float32, (q_heads,), index, "slopes"),
@@ -103,7 +110,7 @@ def kv8_attention_scored(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, scal
     held, wp, wn = _workspace(workspace, need, index, at, cache.device)
     _call("kv8_attention_scored", L.kv8_attention_scored,
           (cache._ref, batch._ref, code, qp, qs, q_heads, rows, cache.scale if scale is None else scale, 1 if causal else 0, window,
-           cap, sp, fp, op, os_, lp, wp, wn), index, at)
+           _cap("kv8_attention_scored", cap), sp, fp, op, os_, lp, wp, wn), index, at)
     return out if lp is None else (out, lse)
 
 
@@ -138,7 +145,7 @@ def kv8_weigh(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, lse: torch.Tens
     held, wp, wn = _workspace(workspace, need, index, at, cache.device)
     _call("kv8_weigh", L.kv8_weigh,
           (cache._ref, batch._ref, code, qp, qs, q_heads, rows, cache.scale if scale is None else scale, 1 if causal else 0, window,
-           cap, sp, fp, lp, mp, wp, wn), index, at)
+           _cap("kv8_weigh", cap), sp, fp, lp, mp, wp, wn), index, at)
 
 
 def kv8_choose(cache: KV8Cache, batch: KV8Batch, mass: torch.Tensor, keep: int, first: int = 0, recent: int = 0, index=None,

@@ -6,6 +6,7 @@ from __future__ import annotations
 import pytest
 
 from ternary_weight_integer_amd import i2s, kv8_scores
+from ternary_weight_integer_amd.i2s import I2SError
 from test_abi_kv8_scores_cpu import FAKE, _batch, _cache, _ref, scored, weigh
 
 
@@ -37,3 +38,12 @@ def test_weigh_without_a_workspace():
     for seqs, rows in ((1, 1), (64, 64), (4, 80)):
         assert weigh_workspace_bytes(_cache(), _batch(starts=None, seqs=seqs), rows) == 0
     assert weigh_workspace_bytes(_cache(dim=120), _batch(), 4096) == weigh_workspace_bytes(_cache(), _batch(), -1) == 0
+
+
+def test_caps_that_round_to_none():
+    """A cap under F32's least number is no cap of 0."""
+    for cap in (1e-50, -1e-50, 2.0 ** -151):
+        with pytest.raises(I2SError) as refused:
+            kv8_scores._cap("kv8_weigh", cap)
+        assert refused.value.status == i2s.I2S_EINVAL
+    assert kv8_scores._cap("kv8_weigh", 0.0) == 0 and kv8_scores._cap("kv8_weigh", 30.0) == 30

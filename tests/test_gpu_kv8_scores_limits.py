@@ -173,3 +173,13 @@ def test_scored_attention_in_a_workspace_of_the_size_asked_for(lens, news):
     got = kv8_scores.kv8_attention_scored(w.cache, w.batch, q, cap=9.0, lse=True, workspace=workspace)
     edge = host(whole)
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and (edge[:256] == 0xFF).all() and (edge[-256:] == 0xFF).all()
+
+
+def test_a_cap_that_rounds_to_none_is_refused():
+    w = World(10, 1, 64, 16, [20], [1])
+    q, lse, mass = dev(w.values(1, F32, heads=2)), torch.zeros((1, 2), device=DEV), kv8_scores.new_mass(w.cache)
+    with pytest.raises(I2SError):
+        kv8_scores.kv8_attention_scored(w.cache, w.batch, q, cap=1e-50)
+    with pytest.raises(I2SError):
+        kv8_scores.kv8_weigh(w.cache, w.batch, q, lse, mass, cap=1e-50)
+    assert not host(mass).any()
