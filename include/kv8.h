@@ -133,7 +133,9 @@ size_t kv8_attention_workspace_bytes(const kv8_cache *cache, const kv8_batch *ba
  *   out = sum_t exp(e_t) * (v_scale * V_t) / sum_t exp(e_t)
  *   lse = log sum_t exp(e_t).
  * Exponents e_t are F32: they resolve to their last bit, and have to stay in
- * its range.
+ * its range.  Queries are held in 22 bits of each component or more, or in 30 of
+ * the row's largest magnitude.  Sums are F32; weights exp(e_t) are multiplied by V
+ * in 22 bits, of many BF16 rows in 11.
  * Value scales below 1e-20 count as 0 (their tokens still do in the sum).
  * A row that sees no token gives zeros and lse = -inf.  A query with a NaN or
  * an infinity gives NaN in its own output row and nowhere else.

@@ -25,6 +25,9 @@
  *   prefix   NULL, or int32 [seqs] (a negative one counts as 0).
  * Exponents e_t and the lse are F32: they resolve to their last bit, and have to
  * stay within +-2^127 (before the cap, where there is one, they need not).
+ * Queries are held as kv8_attention's, in kv8_weigh F32 ones in 22 bits of each
+ * component.  Sums are F32; the attention multiplies weights by V in 22 bits, for
+ * rows of any type.
  * Positions are places in the cache.  After kv8_move they are the places that
  * the chosen tokens then have: windows, distances and prefixes go by those,
  * and rotated keys keep the angles of the positions that they were written at.
@@ -62,7 +65,9 @@ int kv8_attention_scored(const kv8_cache *cache, const kv8_batch *batch, int typ
 size_t kv8_weigh_workspace_bytes(const kv8_cache *cache, const kv8_batch *batch,
                                  int64_t q_heads, int64_t rows);
 
-/* The weight that the batch's rows give each cached token, for each K/V head:
+/* The weight that the batch's rows give each cached token, for each K/V head
+ * (laid out by the sequences' mean number of rows: a prompt's chunk among decode
+ * steps is better a call of its own):
  *   w_t = sum over rows i and the head's query heads h, of those that see t,
  *         of exp(e_t - lse[i][h])
  *   mass_t = w_t for the call's own tokens (those at positions L - n_b and on),

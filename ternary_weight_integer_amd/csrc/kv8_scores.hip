@@ -26,10 +26,10 @@ namespace {
 // Few token blocks are split along their rows into parts of whole stages; the
 // parts' sums are joined in order.
 //
-// A prompt of 4096 F32 rows, 12 heads over 2 of 128: 81 us, 0.31 PFLOP/s of the
-// formula's operations (two f16 a query double them); matrix products take about
-// 21% of the SIMDs' cycles and vector instructions (a weight's scale, exponent and
-// sum, the queries' two parts) 40%, the rest is a workgroup's begin and the
+// A prompt of 4096 F32 rows, 12 heads over 2 of 128: 80 us, 0.32 PFLOP/s of the
+// formula's operations (two f16 a query double them); the matrix units are busy in
+// 27% of the SIMDs' cycles, vector instructions (a weight's scale, exponent and
+// sum, the queries' two parts) in 43%, the rest is a workgroup's begin and the
 // barriers of its stages.  Blocks of 512 tokens (two waves a SIMD, 103 us against
 // then 82) and a tile's operands read ahead (91) were slower.
 
@@ -1066,7 +1066,9 @@ struct WeighPlan {
     // Few rows, up to 32 a sequence and head on average: workgroups that walk
     // several blocks.  64 sequences of 4000 tokens, 8 heads of 128, BF16, with 4, 16,
     // 32, 48 and 64 rows: 47, 49, 62, 77 and 93 us against the other kernel's 55, 56,
-    // 67, 75 and 84.
+    // 67, 75 and 84.  The host knows the mean alone: of 255 sequences with a row
+    // each and one with 1000 that one is a few workgroups' work, and 1540 us pass
+    // (the two apart 107 and 50).
     few = static_cast<int64_t>(s.rows) * (q_heads / c.heads) <= 32 * static_cast<int64_t>(s.seqs);
     if (few && all > kFewGroups * kUnits / each) all = kFewGroups * kUnits / each;
     blocks = all > 1 ? static_cast<int>(all) : 1;
