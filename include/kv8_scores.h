@@ -49,7 +49,7 @@ extern "C" {
 
 /* kv8_attention with shaped scores.  The workspace is
  * kv8_attention_workspace_bytes(...); everything else and the errors are as
- * kv8_attention's (I2S_EINVAL for a cap out of its range, misaligned slopes
+ * kv8_attention's (I2S_EINVAL for a scale or cap out of its range, misaligned slopes
  * or prefix).  A row in front of position 0 sees, where causal, its prefix
  * alone. */
 int kv8_attention_scored(const kv8_cache *cache, const kv8_batch *batch, int type,
